@@ -428,6 +428,170 @@ SS1_API int ss1_bounds_check(int* checked, uint64_t* record);
  */
 SS1_API int ss1_test_bounds_check(int64_t index, int64_t extent);
 
+/*
+ * Operators around the projection. The SS1 pages leave them to the model; the layers' workloads
+ * (GPT-2, BERT, Llama-3-8B) have them in front of, beside and after each projection. None takes a
+ * handle: each runs on the current device, allocates nothing, and keeps nothing between calls, so
+ * calls may run concurrently on any streams and threads as long as they do not share a workspace
+ * or an output. All can be captured into a CUDA graph. Matrices are dense row-major; pointers need
+ * the alignment of their element only (rows and bases on 16-byte boundaries take the faster
+ * kernels). Sums, statistics and products are float32. Outputs must not overlap inputs unless
+ * stated. A NaN or an infinity stays within the outputs that its formula reaches.
+ */
+
+/*
+ * ss1_layernorm_forward -- Y = (X - mean) * rstd * weight + bias over each row of X [M, K], with
+ * mean = sum_k x / K and rstd = 1 / sqrt(sum_k (x - mean)^2 / K + eps).
+ *   X, Y   : device, [M, K] of `dtype`.
+ *   weight, bias : device, [K] of `w_dtype`, or NULL (1, and 0). w_dtype is dtype, or FP32 beside
+ *            bf16 rows.
+ *   mean, rstd : device float [M], written, or NULL; the backward pass reads them.
+ *   eps    : >= 0.
+ * M == 0 is a no-op. The result is rounded once. Asynchronous. Errors: INVALID_ARG (sizes, M or K
+ * past 2^31 - 1 or 2^30, types, NULL X or Y), MISALIGNED (a pointer not aligned to its element), CUDA.
+ */
+SS1_API int ss1_layernorm_forward(const void* X, const void* weight, const void* bias, void* Y, float* mean, float* rstd,
+                                  int64_t M, int64_t K, float eps, int dtype, int w_dtype, void* stream);
+
+/* ss1_layernorm_backward_workspace -- workspace bytes of ss1_layernorm_backward. Errors: INVALID_ARG. */
+SS1_API int ss1_layernorm_backward_workspace(int64_t M, int64_t K, size_t* bytes);
+
+/*
+ * ss1_layernorm_backward -- with xhat = (X - mean) * rstd and g = dY * weight:
+ *     dX = rstd * (g - mean_k(g) - xhat * mean_k(g * xhat)),
+ *     dweight = sum_m dY * xhat,   dbias = sum_m dY.
+ *   dY, X  : device, [M, K] of `dtype` (X as the forward read it).   mean, rstd : float [M], from the forward.
+ *   weight : device, [K] of `w_dtype`, or NULL (1).
+ *   dX     : device, [M, K] of `dtype`, written, or NULL (not computed).
+ *   dweight, dbias : device, [K] of `w_dtype`, overwritten (zero when M == 0), or NULL.
+ *   workspace : device, 16-byte aligned, at least ss1_layernorm_backward_workspace bytes; not
+ *            needed where dweight and dbias are NULL. Calls that share one must be ordered.
+ * The column sums are added in a fixed order: repeated calls give the same bits. Asynchronous.
+ * Errors: as ss1_layernorm_forward; INVALID_ARG for a workspace that is too small.
+ */
+SS1_API int ss1_layernorm_backward(const void* dY, const void* X, const float* mean, const float* rstd, const void* weight,
+                                   void* dX, void* dweight, void* dbias, int64_t M, int64_t K, int dtype, int w_dtype,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside one projection, and their gradients. Row m of a batch
+ * uses adapter a = index[m]; a row whose index is outside [0, count) uses none.
+ *     H[m] = X[m] A[a]^T,   out[m] = Y[m] + scale[a] H[m] B[a]^T   (no adapter: out[m] = Y[m], H[m] = 0)
+ * with Y the projection's output (ss1_forward). For dY, the gradient of out,
+ *     G[m] = scale[a] dY[m] B[a],   dX[m] = dX_in[m] + G[m] A[a],
+ *     dA[a] = sum over its rows of G[m]^T X[m],   dB[a] = scale[a] * sum over its rows of dY[m]^T H[m]
+ * with dX_in the projection's input gradient (ss1_backward_input). Each output is rounded once; H and
+ * G are float32.
+ */
+#define SS1_ADAPTER_MAX_RANK 128
+#define SS1_ADAPTER_MAX_COUNT 1024
+
+typedef struct {
+    const void* A;          /* device, [count, R, K] of dtype                                         */
+    const void* B;          /* device, [count, N, R] of dtype                                         */
+    const float* scale;     /* device, [count], or NULL (1)                                           */
+    const int32_t* index;   /* device, [M], or NULL: every row uses adapter 0 (count must be 1)        */
+    const void* plan;       /* device, what ss1_adapter_plan wrote for the same index, M and count, or NULL:
+                               a call that needs it makes it in its workspace                          */
+    int64_t K, N;           /* 1 .. 2^24 each                                                         */
+    int32_t R;              /* rank, 1 .. SS1_ADAPTER_MAX_RANK                                        */
+    int32_t count;          /* adapters, 1 .. SS1_ADAPTER_MAX_COUNT                                   */
+    int32_t dtype;          /* enum ss1_dtype: X, Y, out, A, B and the gradients                      */
+} ss1_adapters;
+
+/*
+ * ss1_adapter_plan -- the rows of a batch sorted by adapter, for the calls of all layers that run on
+ * that batch. ss1_adapter_plan_bytes: its size for M rows (0 .. 2^30) and `count` adapters.
+ *   index : device int32 [M].   plan : device, 256-byte aligned, written.
+ * Asynchronous. Errors: INVALID_ARG (sizes, NULL, plan too small), MISALIGNED, CUDA.
+ */
+SS1_API int ss1_adapter_plan_bytes(int64_t M, int count, size_t* bytes);
+SS1_API int ss1_adapter_plan(const int32_t* index, int64_t M, int count, void* plan, size_t plan_bytes, void* stream);
+
+/*
+ * ss1_adapter_workspace -- workspace bytes of ss1_adapter_forward and ss1_adapter_backward (either
+ * pointer may be NULL). A workspace is device memory, 256-byte aligned, not read before it is
+ * written; calls that share one must be ordered on the device. Errors: INVALID_ARG.
+ */
+SS1_API int ss1_adapter_workspace(int64_t M, int64_t K, int64_t N, int R, int count, int dtype, size_t* forward_bytes,
+                                  size_t* backward_bytes);
+
+/*
+ * ss1_adapter_forward -- out and, if asked for, H.
+ *   X : device, [M, K].   Y : device, [M, N].   out : device, [M, N], written; may be Y itself.
+ *   H : device float [M, R], written (the backward pass reads it), or NULL.
+ * M == 0 is a no-op. Asynchronous. Errors: INVALID_ARG (sizes, NULL, workspace too small, index NULL
+ * with count > 1), MISALIGNED (a pointer not aligned to its element, plan or workspace not to 256), CUDA.
+ */
+SS1_API int ss1_adapter_forward(const ss1_adapters* adapters, const void* X, const void* Y, void* out, float* H, int64_t M,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ss1_adapter_backward -- dX, dA and dB; each may be NULL (not computed).
+ *   dY : device, [M, N].   X : device, [M, K] (read for dA).   H : device float [M, R], from the
+ *   forward (read for dB).   dX_in : device, [M, K], or NULL (0); may be dX itself.
+ *   dX : [M, K].   dA : [count, R, K].   dB : [count, N, R]; both overwritten, zero for adapters without
+ *   rows.
+ * Sums over rows are added in a fixed order: repeated calls give the same bits. Asynchronous. Errors:
+ * as ss1_adapter_forward.
+ */
+SS1_API int ss1_adapter_backward(const ss1_adapters* adapters, const void* dY, const void* X, const float* H,
+                                 const void* dX_in, void* dX, void* dA, void* dB, int64_t M, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * AdamW (Loshchilov & Hutter, "Decoupled Weight Decay Regularization"), one step over many tensors:
+ *     g' = grad * grad_scale,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps),
+ * each float32 operation rounded on its own. States of 8 bits: blocks of SS1_ADAMW_BLOCK consecutive
+ * elements (the last one of a tensor may be shorter) share one float scale, the smallest power of
+ * two from 2^-126 on that brings the block's largest magnitude to 448 or below; held are OCP FP8
+ * E4M3 codes of m / scale and of sqrt(v) / scale (rounded to nearest even, a positive root at least
+ * to the smallest code). The step uses the new moments before they are rounded.
+ */
+#define SS1_ADAMW_BLOCK 256
+#define SS1_ADAMW_FACTORS 9
+
+typedef struct {
+    void* param;            /* [numel] of param_dtype, updated (written only, where there is a master copy) */
+    const void* grad;       /* [numel] of grad_dtype                                                      */
+    float* master;          /* [numel] float32 copy that the update reads and writes, for bf16 parameters;
+                               NULL: none. param becomes master, rounded                                  */
+    void* exp_avg;          /* m: [numel] float, or E4M3 codes (one byte each)                             */
+    void* exp_avg_sq;       /* v: [numel] float, or E4M3 codes of its root                                */
+    float* avg_scale;       /* 8-bit states: [ceil(numel / SS1_ADAMW_BLOCK)] scales of m; else unused     */
+    float* sq_scale;        /* 8-bit states: the same for the root                                        */
+    int64_t numel;
+    int32_t param_dtype, grad_dtype;   /* enum ss1_dtype, each by itself                                  */
+} ss1_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;           /* number of this step, from 1 on */
+} ss1_adamw_hyper;
+
+/*
+ * ss1_adamw_step -- one step over `count` tensors.
+ *   tensors : host array, read during the call. Tensors must not overlap one another. numel == 0
+ *             is allowed (pointers unused).
+ *   state_bits : 32 or 8, for all tensors. All-zero bytes are a valid start in both.
+ *   hyper   : host; unused where device_factors is given.
+ *   device_factors : NULL, or device float [SS1_ADAMW_FACTORS] as ss1_adamw_factors writes them, read
+ *             when the step runs: a captured step can be replayed with new factors.
+ * Up to 440 tensors run in one launch. Everything is checked before the first launch: a refused
+ * call has changed nothing. Asynchronous. Errors: INVALID_ARG (sizes, types, NULL pointers, a master
+ * copy beside float32 parameters, hyper-parameters out of range: 0 <= beta < 1, eps >= 0, step >= 1,
+ * finite), MISALIGNED (a pointer not aligned to its element), CUDA.
+ */
+SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t count, int state_bits, const ss1_adamw_hyper* hyper,
+                           const float* device_factors, void* stream);
+
+/*
+ * ss1_adamw_factors -- the step's factors in float32, to host memory out[SS1_ADAMW_FACTORS] (no device
+ * is touched). Errors: INVALID_ARG (NULL, hyper-parameters out of range).
+ */
+SS1_API int ss1_adamw_factors(const ss1_adamw_hyper* hyper, float* out);
+
 #ifdef __cplusplus
 }
 #endif

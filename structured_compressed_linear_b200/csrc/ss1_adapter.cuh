@@ -1,0 +1,41 @@
+// Internal declarations of the low-rank adapters' kernels (ss1_adapter.cu).
+#pragma once
+
+#include "ss1_ops.cuh"
+
+namespace ss1 {
+namespace ada {
+
+constexpr int kTile = 128;                               // rows of a tile
+constexpr int kMaxRank = SS1_ADAPTER_MAX_RANK;
+constexpr int kMaxCount = SS1_ADAPTER_MAX_COUNT;
+
+// The rows of a batch by adapter, in device memory: adapter a's rows are rows[first[a] .. first[a + 1]),
+// the rows without one come last (group `count`). tiles: {adapter or -1, first place in rows, rows, 0};
+// those behind the last one have no rows. All null where every row uses adapter 0.
+struct PlanView {
+    int32_t* first;
+    int4* tiles;
+    int32_t* rows;
+    int max_tiles;
+};
+
+inline int max_tiles(int64_t M, int n) { return (int)(M / kTile) + n + 1; }   // each group's last tile may be short
+size_t plan_bytes(int64_t M, int n);
+PlanView plan_view(void* plan, int64_t M, int n);
+cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, cudaStream_t st);
+
+struct Call {
+    const void *A, *B;
+    const float* scale;
+    const int32_t* index;
+    PlanView plan;
+    int64_t M, K, N;
+    int R, n;
+};
+
+// Shares of an adapter's rows in the sums of dA and dB (general path).
+int general_shares(int64_t M, int64_t C, int R, int n);
+
+}  // namespace ada
+}  // namespace ss1

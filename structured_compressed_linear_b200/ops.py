@@ -1,0 +1,456 @@
+"""Binding of the operators around a projection: layer norm, low-rank adapters, AdamW.
+
+The arithmetic runs in the CUDA library (include/ss1.h); this module checks tensors, allocates
+outputs and workspaces, and passes pointers, sizes and the stream. Every call runs on the device
+of its tensors, on `stream` or that device's current stream, and never falls back to another
+implementation. Tensors are contiguous CUDA tensors, bf16 or float32.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import List, Optional, Sequence, Tuple
+
+import numpy as np
+import torch
+
+from . import ss1
+from .ss1 import _check, _dtype_code, lib
+
+#: Limits of the adapters (SS1_ADAPTER_MAX_RANK, SS1_ADAPTER_MAX_COUNT in include/ss1.h).
+ADAPTER_MAX_RANK = 128
+ADAPTER_MAX_COUNT = 1024
+#: Elements that share one scale of an 8-bit AdamW state, and the step's factors (SS1_ADAMW_*).
+ADAMW_BLOCK = 256
+ADAMW_FACTORS = 9
+
+
+def _tensor(name: str, t: torch.Tensor, shape=None, dtype=None, device=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    return t
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+class _On:
+    """The library call's device and stream: makes `device` current for the call where it is not, and
+    ties the tensors that this module allocated to a stream other than the one they came from."""
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self.guard = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = stream
+        self.handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+    def made(self, *tensors):
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _apart(out: torch.Tensor, name: str, **inputs):
+    """A given output must not share memory with an input."""
+    a, b = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for other, t in inputs.items():
+        if t is not None and t.data_ptr() < b and a < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"{name} must not overlap {other}")
+
+
+# ---- layer norm ------------------------------------------------------------------------------
+
+def _norm_weights(X: torch.Tensor, **weights) -> torch.dtype:
+    dt = None
+    for name, w in weights.items():
+        if w is None:
+            continue
+        _tensor(name, w, (X.shape[1],), device=X.device)
+        if w.dtype not in (X.dtype, torch.float32) or (dt is not None and w.dtype != dt):
+            raise ValueError(f"{name} must have X's dtype or float32, and weight and bias one dtype")
+        dt = w.dtype
+    return dt if dt is not None else X.dtype
+
+
+def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                      eps: float = 1e-5, out: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(Y, mean, rstd) of X [M, K]: Y in X's dtype, mean and rstd float32 [M] (ss1_layernorm_forward).
+    weight and bias [K] in X's dtype, or float32 beside bf16 rows."""
+    _tensor("X", X)
+    if X.dim() != 2 or X.shape[1] < 1:
+        raise ValueError("X must be [M, K] with K >= 1")
+    wt = _norm_weights(X, weight=weight, bias=bias)
+    M, K = X.shape
+    on = _On(X.device, stream)
+    if out is None:
+        Y = torch.empty_like(X)
+        on.made(Y)
+    else:
+        Y = _tensor("out", out, X.shape, X.dtype, X.device)
+        _apart(Y, "out", X=X, weight=weight, bias=bias)
+    stats = torch.empty((2, M), dtype=torch.float32, device=X.device)
+    on.made(stats)
+    mean, rstd = stats.unbind(0)
+    with on.guard:
+        _check(lib().ss1_layernorm_forward(X.data_ptr(), _ptr(weight), _ptr(bias), Y.data_ptr(), mean.data_ptr(),
+                                           rstd.data_ptr(), M, K, eps, _dtype_code(X.dtype), _dtype_code(wt), on.handle),
+               "ss1_layernorm_forward")
+    return Y, mean, rstd
+
+
+def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       weight: Optional[torch.Tensor] = None, need: Tuple[bool, bool, bool] = (True, True, True),
+                       stream: Optional[torch.cuda.Stream] = None):
+    """(dX, dweight, dbias) from dY, the forward's X, mean and rstd (ss1_layernorm_backward). dweight and
+    dbias have weight's dtype (X's without a weight). `need`: which of the three to compute (the
+    others are None)."""
+    _tensor("X", X)
+    if X.dim() != 2 or X.shape[1] < 1:
+        raise ValueError("X must be [M, K] with K >= 1")
+    M, K = X.shape
+    _tensor("dY", dY, X.shape, X.dtype, X.device)
+    _tensor("mean", mean, (M,), torch.float32, X.device)
+    _tensor("rstd", rstd, (M,), torch.float32, X.device)
+    wt = _norm_weights(X, weight=weight)
+    on = _On(X.device, stream)
+    dX = torch.empty_like(X) if need[0] else None
+    dw = torch.empty(K, dtype=wt, device=X.device) if need[1] else None
+    db = torch.empty(K, dtype=wt, device=X.device) if need[2] else None
+    ws, size = None, 0
+    L = lib()
+    if need[1] or need[2]:
+        n = ctypes.c_size_t()
+        _check(L.ss1_layernorm_backward_workspace(M, K, ctypes.byref(n)), "ss1_layernorm_backward_workspace")
+        size = n.value
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=X.device)
+    on.made(dX, dw, db, ws)
+    with on.guard:
+        _check(L.ss1_layernorm_backward(dY.data_ptr(), X.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight), _ptr(dX),
+                                        _ptr(dw), _ptr(db), M, K, _dtype_code(X.dtype), _dtype_code(wt), _ptr(ws), size,
+                                        on.handle), "ss1_layernorm_backward")
+    return dX, dw, db
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """Autograd wrapper: Y = LayerNormFunction.apply(X, weight, bias, eps)."""
+
+    @staticmethod
+    def forward(ctx, X, weight, bias, eps=1e-5):
+        X = X.contiguous()
+        Y, mean, rstd = layernorm_forward(X, weight, bias, eps)
+        ctx.save_for_backward(X, mean, rstd, weight)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, mean, rstd, weight = ctx.saved_tensors
+        dX, dw, db = layernorm_backward(dY.contiguous(), X, mean, rstd, weight, tuple(ctx.needs_input_grad[:3]))
+        if db is not None and db.dtype != ctx.bias_dtype:   # a float32 bias without a weight beside bf16 rows
+            db = db.to(ctx.bias_dtype)
+        return dX, dw, db, None
+
+
+# ---- low-rank adapters -----------------------------------------------------------------------
+
+class _Adapters(ctypes.Structure):
+    """ss1_adapters of include/ss1.h."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("plan", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("R", ctypes.c_int32),
+                ("count", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class AdapterPlan:
+    """The rows of a batch sorted by adapter, made once for all layers that run on the batch."""
+
+    def __init__(self, data: torch.Tensor, M: int, count: int):
+        self.data, self.M, self.count = data, M, count
+
+
+def adapter_plan(index: torch.Tensor, count: int, stream: Optional[torch.cuda.Stream] = None) -> AdapterPlan:
+    """Plan of `index` (int32 [M]; outside [0, count): no adapter) for adapter_forward and adapter_backward."""
+    _tensor("index", index, dtype=torch.int32)
+    if index.dim() != 1:
+        raise ValueError("index must be [M]")
+    M, n = index.shape[0], ctypes.c_size_t()
+    L = lib()
+    _check(L.ss1_adapter_plan_bytes(M, count, ctypes.byref(n)), "ss1_adapter_plan_bytes")
+    on = _On(index.device, stream)
+    data = torch.empty(n.value, dtype=torch.uint8, device=index.device)
+    on.made(data)
+    with on.guard:
+        _check(L.ss1_adapter_plan(index.data_ptr(), M, count, data.data_ptr(), n.value, on.handle), "ss1_adapter_plan")
+    return AdapterPlan(data, M, count)
+
+
+def _adapters(X, A, B, index, scale, plan) -> _Adapters:
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("X must be [M, K], A [count, R, K] and B [count, N, R]")
+    M, K = X.shape
+    n, R, _ = A.shape
+    N = B.shape[1]
+    _tensor("X", X)
+    _tensor("A", A, (n, R, K), X.dtype, X.device)
+    _tensor("B", B, (n, N, R), X.dtype, X.device)
+    if not 1 <= R <= ADAPTER_MAX_RANK or not 1 <= n <= ADAPTER_MAX_COUNT:
+        raise ValueError(f"ranks 1 .. {ADAPTER_MAX_RANK} and 1 .. {ADAPTER_MAX_COUNT} adapters, not {R} and {n}")
+    if index is not None:
+        _tensor("index", index, (M,), torch.int32, X.device)
+    elif n != 1:
+        raise ValueError("several adapters need an index")
+    if scale is not None:
+        _tensor("scale", scale, (n,), torch.float32, X.device)
+    if plan is not None:
+        if index is None or plan.M != M or plan.count != n or plan.data.device != X.device:
+            raise ValueError("the plan was made for another batch, count or device")
+    return _Adapters(A.data_ptr(), B.data_ptr(), _ptr(scale), _ptr(index), _ptr(plan.data) if plan is not None else None,
+                     K, N, R, n, _dtype_code(X.dtype))
+
+
+def _adapter_workspace(ad: _Adapters, M: int, backward: bool, device) -> torch.Tensor:
+    n = ctypes.c_size_t()
+    fwd, bwd = (None, ctypes.byref(n)) if backward else (ctypes.byref(n), None)
+    _check(lib().ss1_adapter_workspace(M, ad.K, ad.N, ad.R, ad.count, ad.dtype, fwd, bwd), "ss1_adapter_workspace")
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+
+
+def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.Tensor, index: Optional[torch.Tensor] = None,
+                    scale: Optional[torch.Tensor] = None, keep: bool = False, plan: Optional[AdapterPlan] = None,
+                    out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Y[m] + scale[a] (X[m] A[a]^T) B[a]^T with a = index[m] (ss1_adapter_forward): X [M, K] and the
+    projection's output Y [M, N], A [count, R, K], B [count, N, R], scale float32 [count]. index int32
+    [M]; an entry outside [0, count) leaves its row as it is; None: every row uses the one adapter.
+    `out` may be Y itself. keep: returns (out, H) with H = X A^T, float32 [M, R], for the backward pass."""
+    ad = _adapters(X, A, B, index, scale, plan)
+    M = X.shape[0]
+    _tensor("Y", Y, (M, ad.N), X.dtype, X.device)
+    on = _On(X.device, stream)
+    if out is None:
+        out = torch.empty_like(Y)
+        on.made(out)
+    else:
+        _tensor("out", out, Y.shape, Y.dtype, Y.device)
+        _apart(out, "out", X=X, A=A, B=B, Y=Y if out.data_ptr() != Y.data_ptr() else None)
+    H = torch.empty((M, ad.R), dtype=torch.float32, device=X.device) if keep else None
+    ws = _adapter_workspace(ad, M, False, X.device)
+    on.made(H, ws)
+    with on.guard:
+        _check(lib().ss1_adapter_forward(ctypes.byref(ad), X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
+                                         ws.data_ptr(), ws.numel(), on.handle), "ss1_adapter_forward")
+    return (out, H) if keep else out
+
+
+def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, H: Optional[torch.Tensor],
+                     dX: Optional[torch.Tensor] = None, index: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None, plan: Optional[AdapterPlan] = None,
+                     need: Tuple[bool, bool, bool] = (True, True, True), stream: Optional[torch.cuda.Stream] = None):
+    """(dX, dA, dB) of adapter_forward for dY, the gradient of its output (ss1_adapter_backward). H is what
+    the forward kept (needed for dB); `dX`, if given, is the projection's input gradient, which the
+    result includes. `need`: which of the three to compute (the others are None)."""
+    ad = _adapters(X, A, B, index, scale, plan)
+    M = X.shape[0]
+    _tensor("dY", dY, (M, ad.N), X.dtype, X.device)
+    if need[2]:
+        if H is None:
+            raise ValueError("dB needs H, which adapter_forward(keep=True) returns")
+        _tensor("H", H, (M, ad.R), torch.float32, X.device)
+    if dX is not None:
+        _tensor("dX", dX, X.shape, X.dtype, X.device)
+    on = _On(X.device, stream)
+    out = torch.empty_like(X) if need[0] else None
+    dA = torch.empty_like(A) if need[1] else None
+    dB = torch.empty_like(B) if need[2] else None
+    ws = _adapter_workspace(ad, M, True, X.device)
+    on.made(out, dA, dB, ws)
+    with on.guard:
+        _check(lib().ss1_adapter_backward(ctypes.byref(ad), dY.data_ptr(), X.data_ptr(), _ptr(H) if need[2] else None,
+                                          _ptr(dX) if need[0] else None, _ptr(out), _ptr(dA), _ptr(dB), M, ws.data_ptr(),
+                                          ws.numel(), on.handle), "ss1_adapter_backward")
+    return out, dA, dB
+
+
+class AdaptedSS1Function(torch.autograd.Function):
+    """Autograd wrapper of an SS1 layer with low-rank adapters beside it:
+    Y = AdaptedSS1Function.apply(X, Wc, layer, A, B, index, scale, plan), the last three as in adapter_forward."""
+
+    @staticmethod
+    def forward(ctx, X, Wc, layer, A, B, index=None, scale=None, plan=None):
+        X, Wc, A, B = X.contiguous(), Wc.contiguous(), A.contiguous(), B.contiguous()
+        Y = layer.forward(X, Wc)
+        Y, H = adapter_forward(X, A, B, Y, index, scale, keep=True, plan=plan, out=Y)
+        ctx.layer, ctx.plan = layer, plan
+        ctx.save_for_backward(X, Wc, A, B, H, index, scale)
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, Wc, A, B, H, index, scale = ctx.saved_tensors
+        dY = dY.contiguous()
+        nx, nw, _, na, nb = ctx.needs_input_grad[:5]
+        dX = ctx.layer.backward_input(dY, Wc) if nx else None
+        dWc = ctx.layer.backward_weight(X, dY) if nw else None
+        dA = dB = None
+        if nx or na or nb:
+            dX, dA, dB = adapter_backward(dY, X, A, B, H, dX, index, scale, ctx.plan, (nx, na, nb))
+        return dX, dWc, None, dA, dB, None, None, None
+
+
+# ---- AdamW -----------------------------------------------------------------------------------
+
+class _AdamWHyper(ctypes.Structure):
+    """ss1_adamw_hyper of include/ss1.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+#: ss1_adamw_tensor of include/ss1.h.
+_ADAMW_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("master", "u8"), ("exp_avg", "u8"), ("exp_avg_sq", "u8"),
+                          ("avg_scale", "u8"), ("sq_scale", "u8"), ("numel", "i8"), ("param_dtype", "i4"),
+                          ("grad_dtype", "i4")])
+
+
+def adamw_factors(step: int, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                  weight_decay: float = 0.01, grad_scale: float = 1.0) -> torch.Tensor:
+    """The factors of one step as a float32 CPU tensor [ADAMW_FACTORS] (ss1_adamw_factors). On the device,
+    they are adamw_step's `factors`: a captured step reads them when it is replayed."""
+    out = torch.empty(ADAMW_FACTORS, dtype=torch.float32)
+    h = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
+    _check(lib().ss1_adamw_factors(ctypes.byref(h), out.data_ptr()), "ss1_adamw_factors")
+    return out
+
+
+def _same(name: str, ts: Sequence[torch.Tensor], like: Sequence[torch.Tensor], dtype, device):
+    if len(ts) != len(like):
+        raise ValueError(f"{name}: {len(ts)} tensors for {len(like)} parameters")
+    for t, p in zip(ts, like):
+        if t.numel() != p.numel() or t.device != device or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+            raise ValueError(f"{name} must be contiguous, on {device}, of its parameter's size" +
+                             (f" and {dtype}" if dtype is not None else ""))
+
+
+def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor],
+               exp_avg_sq: Sequence[torch.Tensor], step: int = 1, lr: float = 1e-3,
+               betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+               grad_scale: float = 1.0, master: Optional[Sequence[Optional[torch.Tensor]]] = None,
+               scales: Optional[Tuple[Sequence[torch.Tensor], Sequence[torch.Tensor]]] = None,
+               factors: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """One AdamW step over all tensors, in place (ss1_adamw_step). params and grads: bf16 or float32, each
+    tensor by itself. exp_avg and exp_avg_sq: float32; with `scales` = (of the first moment, of the
+    root of the second one), float32 [ceil(numel / ADAMW_BLOCK)] each, uint8 E4M3 codes instead.
+    master: float32 copies of bf16 params, which the step then reads and writes (None: has none). factors: float32
+    CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale."""
+    n = len(params)
+    if n == 0:
+        return
+    device = params[0].device
+    if device.type != "cuda":
+        raise ValueError("params must be CUDA tensors")
+    bits = 32 if scales is None else 8
+    _same("params", params, params, None, device)
+    _same("grads", grads, params, None, device)
+    state = torch.float32 if bits == 32 else torch.uint8
+    _same("exp_avg", exp_avg, params, state, device)
+    _same("exp_avg_sq", exp_avg_sq, params, state, device)
+    table = np.zeros(n, _ADAMW_TENSOR)
+    ptr = torch.Tensor.data_ptr
+    table["param"], table["grad"] = [ptr(t) for t in params], [ptr(t) for t in grads]
+    table["exp_avg"], table["exp_avg_sq"] = [ptr(t) for t in exp_avg], [ptr(t) for t in exp_avg_sq]
+    table["numel"] = [t.numel() for t in params]
+    table["param_dtype"], table["grad_dtype"] = [_dtype_code(t.dtype) for t in params], [_dtype_code(t.dtype) for t in grads]
+    if master is not None:
+        if len(master) != n:
+            raise ValueError(f"master: {len(master)} tensors for {n} parameters")
+        some = [i for i in range(n) if master[i] is not None]
+        _same("master", [master[i] for i in some], [params[i] for i in some], torch.float32, device)
+        table["master"] = [0 if t is None else ptr(t) for t in master]
+    if scales is not None:
+        for name, ts, field in (("scales[0]", scales[0], "avg_scale"), ("scales[1]", scales[1], "sq_scale")):
+            if len(ts) != n or any(s.numel() != -(-p.numel() // ADAMW_BLOCK) or s.dtype != torch.float32 or s.device != device
+                                   or not s.is_contiguous() for s, p in zip(ts, params)):
+                raise ValueError(f"{name} must be contiguous float32 [ceil(numel / {ADAMW_BLOCK})] a parameter, on {device}")
+            table[field] = [ptr(t) for t in ts]
+    if factors is not None:
+        _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
+    hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
+    on = _On(device, stream)
+    with on.guard:
+        _check(lib().ss1_adamw_step(table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), on.handle), "ss1_adamw_step")
+
+
+class AdamW:
+    """AdamW over a list of parameters: holds the states and calls adamw_step with each parameter's .grad
+    (parameters without one are left as they are).
+
+    state_bits: 32 or 8. master: float32 copies of the bf16 parameters."""
+
+    def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
+        self.params: List[torch.Tensor] = list(params)
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        for i, p in enumerate(self.params):
+            _tensor(f"params[{i}]", p, device=self.params[0].device)
+            _dtype_code(p.dtype)
+            if any(q is p for q in self.params[:i]):
+                raise ValueError(f"params[{i}] is in the list twice")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.steps = state_bits, 0
+        state = torch.float32 if state_bits == 32 else torch.uint8
+        self.exp_avg = [torch.zeros_like(p, dtype=state) for p in self.params]
+        self.exp_avg_sq = [torch.zeros_like(p, dtype=state) for p in self.params]
+        self.scales = None
+        if state_bits == 8:
+            self.scales = tuple([torch.zeros(-(-p.numel() // ADAMW_BLOCK), dtype=torch.float32, device=p.device)
+                                 for p in self.params] for _ in range(2))
+        self.master = [p.detach().float() if master and p.dtype == torch.bfloat16 else None for p in self.params]
+
+    def zero_grad(self):
+        for p in self.params:
+            p.grad = None
+
+    @torch.no_grad()
+    def step(self, grad_scale: float = 1.0, factors: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+        """One step; the step number goes up by one. `factors` as in adamw_step."""
+        who = [i for i, p in enumerate(self.params) if p.grad is not None]
+
+        def of(ts):
+            return [ts[i] for i in who]
+        adamw_step(of(self.params), [self.params[i].grad for i in who], of(self.exp_avg), of(self.exp_avg_sq),
+                   self.steps + 1, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, of(self.master),
+                   None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors, stream)
+        self.steps += 1
+
+    def state_dict(self) -> dict:
+        """States and step number, for a checkpoint (tensors are the live ones)."""
+        return {"steps": self.steps, "state_bits": self.state_bits, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
+                "scales": self.scales, "master": self.master}
+
+    def load_state_dict(self, state: dict):
+        """Copies a state_dict of the same parameters and state_bits back in."""
+        if state["state_bits"] != self.state_bits or len(state["exp_avg"]) != len(self.params):
+            raise ValueError("the state is of other parameters or another state_bits")
+        with torch.no_grad():
+            for mine, theirs in ((self.exp_avg, state["exp_avg"]), (self.exp_avg_sq, state["exp_avg_sq"]),
+                                 (self.master, state["master"])):
+                for a, b in zip(mine, theirs):
+                    if (a is None) != (b is None):
+                        raise ValueError("master copies: one side has one, the other none")
+                    if a is not None:
+                        a.copy_(b)
+            if self.scales is not None:
+                for mine, theirs in zip(self.scales, state["scales"]):
+                    for a, b in zip(mine, theirs):
+                        a.copy_(b)
+        self.steps = state["steps"]
