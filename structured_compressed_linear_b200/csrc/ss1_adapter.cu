@@ -286,7 +286,7 @@ cudaError_t backward_general(const Call& c, const void* dY, const void* X, const
     return e;
 }
 
-size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
+constexpr size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool sizes_ok(int64_t M, int64_t K, int64_t N, int R, int n, int dtype) {
     if (M < 0 || M > (1 << 30) || K < 1 || N < 1 || K > (1 << 24) || N > (1 << 24)) return false;
@@ -294,16 +294,38 @@ bool sizes_ok(int64_t M, int64_t K, int64_t N, int R, int n, int dtype) {
     return (K > N ? K : N) * R * n <= (int64_t)1 << 38;   // what one grid of 256 elements a CTA covers
 }
 
+// The workspaces: the plan, then what the path needs. They hold either path's, so that a workspace's size
+// does not depend on the alignment of the other pointers.
 struct Sizes {
-    size_t plan, rows, part;   // the plan, H or G, the partial sums of dA or dB
+    size_t plan;
+    size_t rows, part;                                  // general path: H or G; the partial sums of dA or dB
+    size_t packed, wide_b, part_a, part_b;              // tensor-core path
+    size_t forward() const { return plan + (rows > packed ? rows : packed); }
+    size_t backward() const {
+        const size_t a = rows + part, b = 2 * packed + wide_b + part_a + part_b;
+        return plan + (a > b ? a : b);
+    }
 };
 Sizes workspace_of(int64_t M, int64_t K, int64_t N, int R, int n) {
-    Sizes s;
+    Sizes s = {};
     s.plan = align_up(plan_bytes(M, n));
     s.rows = align_up((size_t)M * R * sizeof(float));
-    const size_t a = (size_t)general_shares(M, K, R, n) * n * K * R, b = (size_t)general_shares(M, N, R, n) * n * N * R;
-    s.part = align_up((a > b ? a : b) * sizeof(float));
+    const size_t a = (size_t)n * K * R, b = (size_t)n * N * R;
+    const size_t ga = general_shares(M, K, R, n) * a, gb = general_shares(M, N, R, n) * b;
+    s.part = align_up((ga > gb ? ga : gb) * sizeof(float));
+    s.packed = align_up((size_t)M * mma_rank(R) * 2 * sizeof(uint16_t));
+    s.wide_b = R % 8 ? align_up((size_t)n * N * ((R + 7) / 8 * 8) * sizeof(uint16_t)) : 0;
+    const int sa = mma_shares(M, K, n), sb = mma_shares(M, N, n);
+    s.part_a = sa > 1 ? align_up(sa * a * sizeof(float)) : 0;
+    s.part_b = sb > 1 ? align_up(sb * b * sizeof(float)) : 0;
     return s;
+}
+
+// The tensor-core path takes bf16 rows on 16-byte boundaries (and B's rows too, where R allows it), and as
+// many tiles as a grid's second dimension.
+bool mma_shape(const ss1_adapters& ad, int64_t M) {
+    return ad.dtype == SS1_DTYPE_BF16 && ad.K % 8 == 0 && ad.N % 8 == 0 && aligned(ad.A, 16) && (ad.R % 8 || aligned(ad.B, 16)) &&
+           max_tiles(M, ad.count) <= 65535;
 }
 
 // What the calls have in common; `status` other than SS1_OK refuses.
@@ -325,6 +347,16 @@ Call call_of(const ss1_adapters& ad, int64_t M) {
     c.plan = PlanView{};
     return c;
 }
+
+// c.plan: the caller's plan, or one made at `ws`; none where every row uses adapter 0.
+cudaError_t plan_of(const ss1_adapters& ad, int64_t M, void* ws, Call& c, cudaStream_t st) {
+    if (!ad.index) return cudaSuccess;
+    c.plan = plan_view(ad.plan ? const_cast<void*>(ad.plan) : ws, M, ad.count);
+    return ad.plan ? cudaSuccess : launch_plan(ad.index, M, ad.count, c.plan, st);
+}
+
+// Rows up to which the general kernels serve bf16 calls too.
+constexpr int64_t kGeneralRows = 32;
 
 }  // namespace
 
@@ -377,8 +409,8 @@ extern "C" SS1_API int ss1_adapter_workspace(int64_t M, int64_t K, int64_t N, in
                                              size_t* backward_bytes) {
     if (!sizes_ok(M, K, N, R, count, dtype)) return SS1_ERR_INVALID_ARG;
     const Sizes s = workspace_of(M, K, N, R, count);
-    if (forward_bytes) *forward_bytes = s.plan + s.rows;
-    if (backward_bytes) *backward_bytes = s.plan + s.rows + s.part;
+    if (forward_bytes) *forward_bytes = s.forward();
+    if (backward_bytes) *backward_bytes = s.backward();
     return SS1_OK;
 }
 
@@ -390,11 +422,19 @@ extern "C" SS1_API int ss1_adapter_forward(const ss1_adapters* ad, const void* X
     const size_t e = dtype_size(ad->dtype);
     if (!aligned(X, e) || !aligned(Y, e) || !aligned(out, e) || !aligned(H, 4) || !aligned(workspace, 256)) return SS1_ERR_MISALIGNED;
     const Sizes s = workspace_of(M, ad->K, ad->N, ad->R, ad->count);
-    if (!workspace || workspace_bytes < s.plan + s.rows) return SS1_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < s.forward()) return SS1_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     Call c = call_of(*ad, M);
-    if (!H) H = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.plan);
-    const cudaError_t err = ad->dtype == SS1_DTYPE_BF16 ? forward_general<__nv_bfloat16>(c, X, Y, out, H, st)
+    cudaError_t err = cudaSuccess;
+    if (M > kGeneralRows && mma_shape(*ad, M) && aligned(X, 16) && aligned(Y, 16) && aligned(out, 16)) {
+        err = plan_of(*ad, M, ws, c, st);
+        if (err == cudaSuccess) err = mma_forward(c, X, Y, out, H, ws + s.plan, st);
+        if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
+        return SS1_OK;
+    }
+    if (!H) H = reinterpret_cast<float*>(ws + s.plan);
+    err = ad->dtype == SS1_DTYPE_BF16 ? forward_general<__nv_bfloat16>(c, X, Y, out, H, st)
                                                         : forward_general<float>(c, X, Y, out, H, st);
     if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
     return SS1_OK;
@@ -420,12 +460,22 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
     if (!dX && !dA && !dB) return SS1_OK;
     if (!dY || (dA && !X) || (dB && !H) || (dX_in && !dX)) return SS1_ERR_INVALID_ARG;
     const Sizes s = workspace_of(M, ad->K, ad->N, ad->R, ad->count);
-    if (!workspace || workspace_bytes < s.plan + s.rows + s.part) return SS1_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < s.backward()) return SS1_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     Call c = call_of(*ad, M);
-    if (ad->index) {
-        c.plan = plan_view(ad->plan ? const_cast<void*>(ad->plan) : ws, M, ad->count);
-        if (!ad->plan) err = launch_plan(ad->index, M, ad->count, c.plan, st);
+    err = plan_of(*ad, M, ws, c, st);
+    if (err == cudaSuccess && M > kGeneralRows && mma_shape(*ad, M) && aligned(dY, 16) && aligned(X, 16) && aligned(dX_in, 16) &&
+        aligned(dX, 16)) {
+        uint8_t* at = ws + s.plan;
+        MmaSpace w;
+        w.packed_h = at; at += s.packed;
+        w.packed_g = at; at += s.packed;
+        w.wide_b = at; at += s.wide_b;
+        w.part_a = reinterpret_cast<float*>(at); at += s.part_a;
+        w.part_b = reinterpret_cast<float*>(at);
+        err = mma_backward(c, dY, X, H, dX_in, dX, dA, dB, w, st);
+        if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
+        return SS1_OK;
     }
     float* G = reinterpret_cast<float*>(ws + s.plan);
     float* part = reinterpret_cast<float*>(ws + s.plan + s.rows);

@@ -37,5 +37,17 @@ struct Call {
 // Shares of an adapter's rows in the sums of dA and dB (general path).
 int general_shares(int64_t M, int64_t C, int R, int n);
 
+// Tensor-core path (ss1_adapter_mma.cu): bf16, K and N multiples of 8, 16-byte aligned rows.
+struct MmaSpace {
+    void *packed_h, *packed_g;   // [M][2][mma_rank(R)] bf16: s H and G in plan order, two parts each
+    void* wide_b;                // B with rows of a multiple of 8 elements, where R is none
+    float *part_a, *part_b;      // the shares' partial dA and dB
+};
+int mma_rank(int R);                             // R as the kernels pad it
+int mma_shares(int64_t M, int64_t C, int n);     // shares of the rows in dA or dB with C columns
+cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, void* packed, cudaStream_t st);
+cudaError_t mma_backward(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
+                         const MmaSpace& w, cudaStream_t st);
+
 }  // namespace ada
 }  // namespace ss1
