@@ -28,28 +28,40 @@ using namespace op;
 
 // One CTA. Every warp counts its own contiguous share of the rows by adapter (lanes with the same
 // adapter find one another by __match_any_sync), the counts are scanned over adapters and warps,
-// and the same walk again gives each row its place: rows keep their order within an adapter.
+// and the same walk again gives each row its place: rows keep their order within an adapter. The
+// first kAhead index words of a lane are loaded together and kept for the second walk (32 warps
+// cover 16,384 rows that way): one memory latency instead of one for every 32 rows, twice.
+constexpr int kAhead = 16;
+
+__device__ __forceinline__ int plan_group(const int32_t* __restrict__ index, int row, int end, int n) {
+    if (row >= end) return -1;
+    const int a = index[row];
+    return (unsigned)a < (unsigned)n ? a : n;
+}
+
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ index, int M, int n, PlanView plan) {
-    extern __shared__ int cnt[];   // [warps][n + 1], then [n + 2] first rows
+    extern __shared__ int cnt[];   // [warps][n + 1], then [n + 2] first rows and [n + 2] first tiles
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int groups = n + 1;      // group n: rows without an adapter
     int* first = cnt + warps * groups;
-    for (int i = threadIdx.x; i < warps * groups; i += blockDim.x) cnt[i] = 0;
-    __syncthreads();
+    int* first_tile = first + n + 2;
     const int share = (M + warps - 1) / warps;
     const int begin = min(M, warp * share), end = min(M, begin + share);
+    int ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = plan_group(index, begin + i * 32 + lane, end, n);
+    for (int i = threadIdx.x; i < warps * groups; i += blockDim.x) cnt[i] = 0;
+    __syncthreads();
     int* mine = cnt + warp * groups;
-    for (int at = begin; at < end; at += 32) {
-        const int row = at + lane;
-        int a = -1;
-        if (row < end) {
-            a = index[row];
-            if ((unsigned)a >= (unsigned)n) a = n;
-        }
+    auto count = [&](int a) {
         const unsigned same = __match_any_sync(0xFFFFFFFFu, a);
         if (a >= 0 && lane == __ffs(same) - 1) mine[a] += __popc(same);
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (begin + i * 32 < end) count(ahead[i]);
+    for (int at = begin + kAhead * 32; at < end; at += 32) count(plan_group(index, at + lane, end, n));
     __syncthreads();
     // totals, then their exclusive sums (one warp, 32 groups at a time), with the tiles' beside them
     for (int a = threadIdx.x; a < groups; a += blockDim.x) {
@@ -76,44 +88,57 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
             }
             if (a < groups) {
                 first[a] = rows + cs - c;
-                plan.first[a] = rows + cs - c;
-                for (int i = 0; i < t; ++i) {
-                    const int at_tile = tiles + ts - t + i;
-                    if (SS1_IN(at_tile, plan.max_tiles, kSitePlan))
-                        plan.tiles[at_tile] = make_int4(a < n ? a : -1, rows + cs - c + i * kTile, min(kTile, c - i * kTile), 0);
-                }
+                first_tile[a] = tiles + ts - t;
             }
             rows += __shfl_sync(0xFFFFFFFFu, cs, 31);
             tiles += __shfl_sync(0xFFFFFFFFu, ts, 31);
         }
-        if (lane == 0) plan.first[groups] = rows;
-        for (int i = tiles + lane; i < plan.max_tiles; i += 32) plan.tiles[i] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) {
+            first[groups] = rows;
+            first_tile[groups] = tiles;
+        }
     }
     __syncthreads();
-    for (int at = begin; at < end; at += 32) {
-        const int row = at + lane;
-        int a = -1;
-        if (row < end) {
-            a = index[row];
-            if ((unsigned)a >= (unsigned)n) a = n;
+    for (int a = threadIdx.x; a <= groups; a += blockDim.x) {
+        plan.first[a] = first[a];
+        plan.first_tile[a] = first_tile[a];
+    }
+    for (int i = threadIdx.x; i < plan.max_tiles; i += blockDim.x) {
+        int4 t = make_int4(-1, 0, 0, 0);
+        if (i < first_tile[groups]) {
+            int lo = 0, hi = groups - 1;               // the last group whose first tile is at or before i and that has rows
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (first_tile[mid] <= i) lo = mid;
+                else hi = mid - 1;
+            }
+            const int at = first[lo] + (i - first_tile[lo]) * kTile;
+            t = make_int4(lo < n ? lo : -1, at, min(kTile, first[lo + 1] - at), 0);
         }
+        plan.tiles[i] = t;
+    }
+    auto place = [&](int a, int row) {
         const unsigned same = __match_any_sync(0xFFFFFFFFu, a);
-        int place = 0;
-        if (a >= 0) place = first[a] + mine[a] + __popc(same & ((1u << lane) - 1u));
+        int to = 0;
+        if (a >= 0) to = first[a] + mine[a] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
         if (a >= 0) {
             if (lane == __ffs(same) - 1) mine[a] += __popc(same);
-            if (SS1_IN(place, M, kSitePlan)) plan.rows[place] = row;
+            if (SS1_IN(to, M, kSitePlan)) plan.rows[to] = row;
         }
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (begin + i * 32 < end) place(ahead[i], begin + i * 32 + lane);
+    for (int at = begin + kAhead * 32; at < end; at += 32) place(plan_group(index, at + lane, end, n), at + lane);
 }
 
 cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, cudaStream_t st) {
     // counters of every warp beside one another in the 48 KB that need no opt-in
-    int warps = (int)((48 * 1024 / 4 - (n + 2)) / (n + 1));
+    int warps = (48 * 1024 / 4 - 2 * (n + 2)) / (n + 1);
     warps = warps > 32 ? 32 : warps;
-    const size_t smem = ((size_t)warps * (n + 1) + n + 2) * sizeof(int);
+    const size_t smem = ((size_t)warps * (n + 1) + 2 * (n + 2)) * sizeof(int);
     plan_kernel<<<1, warps * 32, smem, st>>>(index, (int)M, n, plan);
     return cudaGetLastError();
 }
@@ -299,10 +324,10 @@ bool sizes_ok(int64_t M, int64_t K, int64_t N, int R, int n, int dtype) {
 struct Sizes {
     size_t plan;
     size_t rows, part;                                  // general path: H or G; the partial sums of dA or dB
-    size_t packed, wide_b, part_a, part_b;              // tensor-core path
-    size_t forward() const { return plan + (rows > packed ? rows : packed); }
+    size_t packed, wide_b, turned_a, part_a, part_b;    // tensor-core path
+    size_t forward() const { return plan + (rows > packed + wide_b ? rows : packed + wide_b); }
     size_t backward() const {
-        const size_t a = rows + part, b = 2 * packed + wide_b + part_a + part_b;
+        const size_t a = rows + part, b = 2 * packed + wide_b + turned_a + part_a + part_b;
         return plan + (a > b ? a : b);
     }
 };
@@ -315,9 +340,9 @@ Sizes workspace_of(int64_t M, int64_t K, int64_t N, int R, int n) {
     s.part = align_up((ga > gb ? ga : gb) * sizeof(float));
     s.packed = align_up((size_t)M * mma_rank(R) * 2 * sizeof(uint16_t));
     s.wide_b = R % 8 ? align_up((size_t)n * N * ((R + 7) / 8 * 8) * sizeof(uint16_t)) : 0;
-    const int sa = mma_shares(M, K, n), sb = mma_shares(M, N, n);
-    s.part_a = sa > 1 ? align_up(sa * a * sizeof(float)) : 0;
-    s.part_b = sb > 1 ? align_up(sb * b * sizeof(float)) : 0;
+    s.turned_a = align_up((size_t)n * K * ((R + 7) / 8 * 8) * sizeof(uint16_t));
+    s.part_a = align_up((size_t)(mma_runs(M, K, n) + n) * K * R * sizeof(float));
+    s.part_b = align_up((size_t)(mma_runs(M, N, n) + n) * N * R * sizeof(float));
     return s;
 }
 
@@ -369,14 +394,15 @@ int general_shares(int64_t M, int64_t C, int R, int n) {
 }
 
 size_t plan_bytes(int64_t M, int n) {
-    return ((size_t)(n + 2 + 3) / 4 * 4 + 4 * (size_t)max_tiles(M, n) + (size_t)M) * sizeof(int32_t);
+    return (2 * ((size_t)(n + 2 + 3) / 4 * 4) + 4 * (size_t)max_tiles(M, n) + (size_t)M) * sizeof(int32_t);
 }
 
 PlanView plan_view(void* plan, int64_t M, int n) {
     PlanView v;
     v.first = static_cast<int32_t*>(plan);
     v.max_tiles = max_tiles(M, n);
-    v.tiles = reinterpret_cast<int4*>(v.first + (n + 2 + 3) / 4 * 4);
+    v.first_tile = v.first + (n + 2 + 3) / 4 * 4;
+    v.tiles = reinterpret_cast<int4*>(v.first_tile + (n + 2 + 3) / 4 * 4);
     v.rows = reinterpret_cast<int32_t*>(v.tiles + v.max_tiles);
     return v;
 }
@@ -429,7 +455,8 @@ extern "C" SS1_API int ss1_adapter_forward(const ss1_adapters* ad, const void* X
     cudaError_t err = cudaSuccess;
     if (M > kGeneralRows && mma_shape(*ad, M) && aligned(X, 16) && aligned(Y, 16) && aligned(out, 16)) {
         err = plan_of(*ad, M, ws, c, st);
-        if (err == cudaSuccess) err = mma_forward(c, X, Y, out, H, ws + s.plan, st);
+        const MmaSpace w{ws + s.plan, nullptr, ws + s.plan + s.packed, nullptr, nullptr, nullptr};
+        if (err == cudaSuccess) err = mma_forward(c, X, Y, out, H, w, st);
         if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
         return SS1_OK;
     }
@@ -468,9 +495,10 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
         aligned(dX, 16)) {
         uint8_t* at = ws + s.plan;
         MmaSpace w;
-        w.packed_h = at; at += s.packed;
         w.packed_g = at; at += s.packed;
+        w.packed_h = at; at += s.packed;
         w.wide_b = at; at += s.wide_b;
+        w.turned_a = at; at += s.turned_a;
         w.part_a = reinterpret_cast<float*>(at); at += s.part_a;
         w.part_b = reinterpret_cast<float*>(at);
         err = mma_backward(c, dY, X, H, dX_in, dX, dA, dB, w, st);

@@ -12,9 +12,11 @@ constexpr int kMaxCount = SS1_ADAPTER_MAX_COUNT;
 
 // The rows of a batch by adapter, in device memory: adapter a's rows are rows[first[a] .. first[a + 1]),
 // the rows without one come last (group `count`). tiles: {adapter or -1, first place in rows, rows, 0};
-// those behind the last one have no rows. All null where every row uses adapter 0.
+// adapter a's are tiles[first_tile[a] .. first_tile[a + 1]), those behind the last one have no rows. All
+// null where every row uses adapter 0.
 struct PlanView {
-    int32_t* first;
+    int32_t* first;         // [count + 2]
+    int32_t* first_tile;    // [count + 2]
     int4* tiles;
     int32_t* rows;
     int max_tiles;
@@ -39,13 +41,14 @@ int general_shares(int64_t M, int64_t C, int R, int n);
 
 // Tensor-core path (ss1_adapter_mma.cu): bf16, K and N multiples of 8, 16-byte aligned rows.
 struct MmaSpace {
-    void *packed_h, *packed_g;   // [M][2][mma_rank(R)] bf16: s H and G in plan order, two parts each
+    void *packed_g, *packed_h;   // [M][2][mma_rank(R)] bf16 in plan order, two parts each: s H (forward) or G; s H beside it
     void* wide_b;                // B with rows of a multiple of 8 elements, where R is none
-    float *part_a, *part_b;      // the shares' partial dA and dB
+    void* turned_a;              // A transposed, [count][K][R rounded up to 8]
+    float *part_a, *part_b;      // the runs' partial dA and dB
 };
 int mma_rank(int R);                             // R as the kernels pad it
-int mma_shares(int64_t M, int64_t C, int n);     // shares of the rows in dA or dB with C columns
-cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, void* packed, cudaStream_t st);
+int mma_runs(int64_t M, int64_t C, int n);       // runs of tiles in dA or dB with C columns
+cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st);
 cudaError_t mma_backward(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
                          const MmaSpace& w, cudaStream_t st);
 

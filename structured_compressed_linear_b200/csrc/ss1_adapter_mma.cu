@@ -60,12 +60,80 @@ struct Tile {
 __device__ __forceinline__ Tile tile_of(const PlanView& plan, int i, int M) {
     if (plan.rows == nullptr) return Tile{0, i * kTile, min(kTile, M - i * kTile)};
     const int4 t = plan.tiles[i];
-    return Tile{t.x, t.y, min(t.z, M - t.y)};   // a plan of another batch cannot lead past M places
+    return Tile{t.x, t.y, t.y < 0 ? 0 : min(t.z, min(kTile, M - t.y))};   // a plan of another batch leads to no other places
 }
 // The batch row at a place of the plan, -1 if there is none.
 __device__ __forceinline__ int row_at(const PlanView& plan, int place, int M) {
     const int m = plan.rows == nullptr ? place : plan.rows[place];
     return (unsigned)m < (unsigned)M ? m : -1;
+}
+
+// ---- prepare ---------------------------------------------------------------------------------
+
+// What the other kernels read in another form, in one launch: CTAs 0 .. nh - 1 pack the caller's H, then
+// nb widen B's rows to a multiple of 8 elements, the rest transpose A 32 x 32 at a time.
+struct Prepare {
+    const float* H;            // [M, R] -> packed_h, scaled
+    const int32_t* index;
+    const float* scale;
+    bf16* packed_h;
+    const bf16* B;             // [b_rows, R] -> wide_b [b_rows, ld]
+    bf16* wide_b;
+    int64_t b_rows;
+    const bf16* A;             // [count, R, K] -> turned_a [count, K, ld]
+    bf16* turned_a;
+    int K, ld;
+    int nh, nb, na;            // CTAs of each part
+};
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, PlanView plan, int M, int R, int n) {
+    __shared__ bf16 box[32][33];
+    let_next_start();
+    const int tid = threadIdx.x;
+    int cta = blockIdx.x;
+    if (cta < d.nh) {
+        const int64_t pairs = (int64_t)M * (RT / 2);
+        for (int64_t i = (int64_t)cta * kThreads + tid; i < pairs; i += (int64_t)d.nh * kThreads) {
+            const int place = (int)(i / (RT / 2)), c = (int)(i % (RT / 2)) * 2;
+            const int m = row_at(plan, place, M);
+            const int a = m >= 0 && d.index ? d.index[m] : 0;
+            const bool some = m >= 0 && (unsigned)a < (unsigned)n;
+            const float f = some && d.scale ? d.scale[a] : 1.0f;
+            uint32_t hi, lo;
+            split2(some && c < R ? f * d.H[(int64_t)m * R + c] : 0.0f, some && c + 1 < R ? f * d.H[(int64_t)m * R + c + 1] : 0.0f, hi, lo);
+            if (!SS1_SPAN_IN((int64_t)place * 2 * RT + RT + c, 2, (int64_t)M * 2 * RT, kSiteAdaG)) continue;
+            *reinterpret_cast<uint32_t*>(d.packed_h + (int64_t)place * 2 * RT + c) = hi;
+            *reinterpret_cast<uint32_t*>(d.packed_h + (int64_t)place * 2 * RT + RT + c) = lo;
+        }
+        return;
+    }
+    cta -= d.nh;
+    if (cta < d.nb) {
+        const int64_t size = d.b_rows * d.ld;
+        for (int64_t i = (int64_t)cta * kThreads + tid; i < size; i += (int64_t)d.nb * kThreads) {
+            const int64_t row = i / d.ld;
+            const int r = (int)(i - row * d.ld);
+            d.wide_b[i] = r < R && SS1_IN(row * R + r, d.b_rows * R, kSiteAdaB) ? d.B[row * R + r] : __float2bfloat16_rn(0.0f);
+        }
+        return;
+    }
+    cta -= d.nb;
+    const int kb = (d.K + 31) / 32, rb = (d.ld + 31) / 32;
+    for (int64_t i = cta; i < (int64_t)kb * rb * n; i += d.na) {
+        const int k0 = (int)(i % kb) * 32, r0 = (int)(i / kb % rb) * 32, a = (int)(i / kb / rb);
+        __syncthreads();
+        for (int y = tid / 32; y < 32; y += kThreads / 32) {
+            const int k = k0 + tid % 32, r = r0 + y;
+            const int64_t at = ((int64_t)a * R + r) * d.K + k;
+            box[y][tid % 32] = r < R && k < d.K && SS1_IN(at, (int64_t)n * R * d.K, kSiteAdaA) ? d.A[at] : __float2bfloat16_rn(0.0f);
+        }
+        __syncthreads();
+        for (int y = tid / 32; y < 32; y += kThreads / 32) {
+            const int k = k0 + y, r = r0 + tid % 32;
+            if (k < d.K && r < d.ld) d.turned_a[((int64_t)a * d.K + k) * d.ld + r] = box[tid % 32][y];
+        }
+    }
 }
 
 // ---- products --------------------------------------------------------------------------------
@@ -92,11 +160,11 @@ struct ProductsShape {
 template <int RT, bool TRANS>
 __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restrict__ U, const bf16* __restrict__ table, int ld,
                                                             const float* __restrict__ scale, PlanView plan, float* __restrict__ H,
-                                                            bf16* __restrict__ packed, bool scale_packed, int M, int C, int R,
-                                                            int n) {
+                                                            bf16* __restrict__ packed, int M, int C, int R, int n) {
     using S = ProductsShape<RT, TRANS>;
     extern __shared__ uint8_t raw[];
     let_next_start();
+    wait_for_previous();   // the prepared B; all of this grid waits, so that the next one need not look further back
     const Tile tile = tile_of(plan, blockIdx.y, M);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int splits = gridDim.x, split = blockIdx.x;
@@ -114,38 +182,50 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
     const int chunks = (C + 63) / 64, per = (chunks + splits - 1) / splits;
     const int from = min(chunks, split * per), to = min(chunks, from + per);
 
-    // this thread's four rows of a stage: one 16-byte chunk of each
-    const bf16* urow[4];
+    // this thread's pieces of a stage: a 16-byte chunk of four rows of U, and its share of T. Addresses and
+    // predicates are worked out here; a stage adds one stride to each.
     const int uc = tid % 8;
+    const bf16* up[4];
+    bool uok[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = tid / 8 + 32 * i;
         const int m = r < tile.rows ? row_at(plan, tile.first + r, M) : -1;
-        urow[i] = m >= 0 ? U + (int64_t)m * C : nullptr;
+        uok[i] = m >= 0;
+        up[i] = U + (m >= 0 ? (int64_t)m * C : 0) + (int64_t)from * 64 + uc * 8;
     }
-    auto load = [&](int chunk, int slot) {
-        if (chunk < to) {
-            const uint32_t su = base + slot * S::stage, stt = su + S::u_bytes;
-            const int c0 = chunk * 64;
+    constexpr int kPieces = TRANS ? 64 * (RT / 8) : RT * 8, kMine = (kPieces + kThreads - 1) / kThreads;
+    const bf16* tp[kMine];
+    bool tok[kMine];
+    uint32_t tdst[kMine];
+    int tcol[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int k = tid + i * kThreads;
+        const int c = TRANS ? k / (RT / 8) : (k % 8) * 8, r = TRANS ? (k % (RT / 8)) * 8 : k / 8;
+        tok[i] = k < kPieces && r < (TRANS ? ld : R);
+        tcol[i] = from * 64 + c;
+        tp[i] = T + (tok[i] ? (TRANS ? (int64_t)tcol[i] * ld + r : (int64_t)r * C + tcol[i]) : 0);
+        tdst[i] = S::u_bytes + (TRANS ? c * S::t_pitch + r * 2 : r * 128 + (((k % 8) ^ (r & 7)) << 4));
+    }
+    int ucol = from * 64 + uc * 8;
+    auto load = [&](bool some, int slot) {      // the next stage in line
+        if (some) {
+            const uint32_t su = base + slot * S::stage;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = tid / 8 + 32 * i, c = c0 + uc * 8;
-                const bool ok = urow[i] && c < C && SS1_SPAN_IN(urow[i] + c - U, 8, (int64_t)M * C, kSiteAdaX);
-                copy16(su + r * 128 + ((uc ^ (r & 7)) << 4), ok ? urow[i] + c : U, ok);
+                const int r = tid / 8 + 32 * i;
+                const bool ok = uok[i] && ucol < C && SS1_SPAN_IN(up[i] - U, 8, (int64_t)M * C, kSiteAdaX);
+                copy16(su + r * 128 + ((uc ^ (r & 7)) << 4), ok ? up[i] : U, ok);
+                up[i] += 64;
             }
-            if (TRANS) {
-                constexpr int cw = RT / 8;
-                for (int i = tid; i < 64 * cw; i += kThreads) {
-                    const int c = c0 + i / cw, r = (i % cw) * 8;
-                    const bool ok = c < C && r < ld && SS1_SPAN_IN(T + (int64_t)c * ld + r - table, 8, (int64_t)n * C * ld, kSiteAdaB);
-                    copy16(stt + (i / cw) * S::t_pitch + r * 2, ok ? T + (int64_t)c * ld + r : table, ok);
-                }
-            } else {
-                for (int i = tid; i < RT * 8; i += kThreads) {
-                    const int r = i / 8, c = c0 + (i % 8) * 8;
-                    const bool ok = r < R && c < C && SS1_SPAN_IN(T + (int64_t)r * C + c - table, 8, (int64_t)n * C * R, kSiteAdaA);
-                    copy16(stt + r * 128 + (((i % 8) ^ (r & 7)) << 4), ok ? T + (int64_t)r * C + c : table, ok);
-                }
+            ucol += 64;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const bool ok = tok[i] && tcol[i] < C && SS1_SPAN_IN(tp[i] - table, 8, (int64_t)n * C * (TRANS ? ld : R), kSiteAdaA);
+                if (kPieces % kThreads == 0 || tid + i * kThreads < kPieces) copy16(su + tdst[i], ok ? tp[i] : table, ok);
+                tp[i] += TRANS ? (int64_t)64 * ld : 64;
+                tcol[i] += 64;
             }
         }
         ptx::cp_async_commit();
@@ -156,43 +236,48 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
     for (int j = 0; j < RT / 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[j][i] = 0.0f;
-    for (int s = 0; s < kStages - 1; ++s) load(from + s, s);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load(from + s < to, s);
     const bool busy = warp * 16 < tile.rows;
-    for (int chunk = from; chunk < to; ++chunk) {
-        ptx::cp_async_wait<kStages - 2>();
-        __syncthreads();
-        load(chunk + kStages - 1, (chunk - from + kStages - 1) % kStages);
-        if (!busy) continue;
-        const uint32_t su = base + ((chunk - from) % kStages) * S::stage, stt = su + S::u_bytes;
-        float acc[RT / 8][4];
+    for (int first = from; first < to; first += kStages)
 #pragma unroll
-        for (int j = 0; j < RT / 8; ++j)
+        for (int s = 0; s < kStages; ++s) {
+            const int chunk = first + s;
+            if (chunk >= to) break;
+            ptx::cp_async_wait<kStages - 2>();
+            __syncthreads();
+            load(chunk + kStages - 1 < to, (s + kStages - 1) % kStages);
+            if (!busy) continue;
+            const uint32_t su = base + s * S::stage, stt = su + S::u_bytes;
+            float acc[RT / 8][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+            for (int j = 0; j < RT / 8; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t a[4];
-            const int ar = warp * 16 + lane % 16;
-            ldsm4(a, su + ar * 128 + (((k * 2 + lane / 16) ^ (ar & 7)) << 4));
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < RT / 8; j += 2) {
-                uint32_t b[4];
-                const int mat = lane / 8, l8 = lane % 8;
-                if (TRANS) {
-                    ldsm4_trans(b, stt + (k * 16 + (mat % 2) * 8 + l8) * S::t_pitch + (j + mat / 2) * 16);
-                } else {
-                    const int r = (j + mat / 2) * 8 + l8;
-                    ldsm4(b, stt + r * 128 + (((k * 2 + mat % 2) ^ (r & 7)) << 4));
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a[4];
+                const int ar = warp * 16 + lane % 16;
+                ldsm4(a, su + ar * 128 + (((k * 2 + lane / 16) ^ (ar & 7)) << 4));
+#pragma unroll
+                for (int j = 0; j < RT / 8; j += 2) {
+                    uint32_t b[4];
+                    const int mat = lane / 8, l8 = lane % 8;
+                    if (TRANS) {
+                        ldsm4_trans(b, stt + (k * 16 + (mat % 2) * 8 + l8) * S::t_pitch + (j + mat / 2) * 16);
+                    } else {
+                        const int r = (j + mat / 2) * 8 + l8;
+                        ldsm4(b, stt + r * 128 + (((k * 2 + mat % 2) ^ (r & 7)) << 4));
+                    }
+                    mma16816(acc[j], a, b[0], b[1]);
+                    mma16816(acc[j + 1], a, b[2], b[3]);
                 }
-                mma16816(acc[j], a, b[0], b[1]);
-                mma16816(acc[j + 1], a, b[2], b[3]);
             }
+#pragma unroll
+            for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[j][i] += acc[j][i];
         }
-#pragma unroll
-        for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[j][i] += acc[j][i];
-    }
     ptx::cp_async_wait<0>();
     __syncthreads();
     // the partial products over the ring's memory
@@ -225,7 +310,8 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
             if (c < R) H[(int64_t)m * R + c] = x;
             if (c + 1 < R) H[(int64_t)m * R + c + 1] = y;
         }
-        if (scale_packed) { x *= f; y *= f; }
+        x *= f;
+        y *= f;
         uint32_t hi, lo;
         split2(x, y, hi, lo);
         if (SS1_SPAN_IN((int64_t)place * 2 * RT + RT + c, 2, (int64_t)M * 2 * RT, kSiteAdaG)) {
@@ -236,102 +322,132 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
     if (splits > 1) ptx::cluster_sync();   // nobody leaves while its sums are being read
 }
 
-// packed[i] = scale[a] H[rows[i]] in two parts, for an H that the caller brings.
-template <int RT>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const float* __restrict__ H, const int32_t* __restrict__ index,
-                                                        const float* __restrict__ scale, PlanView plan, bf16* __restrict__ packed,
-                                                        int M, int R, int n) {
-    let_next_start();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int place = (int)(i / (RT / 2)), c = (int)(i % (RT / 2)) * 2;
-    if (place >= M) return;
-    const int m = row_at(plan, place, M);
-    const int a = m >= 0 && index ? index[m] : 0;
-    const bool some = m >= 0 && (unsigned)a < (unsigned)n;
-    const float f = some && scale ? scale[a] : 1.0f;
-    uint32_t hi, lo;
-    split2(some && c < R ? f * H[(int64_t)m * R + c] : 0.0f, some && c + 1 < R ? f * H[(int64_t)m * R + c + 1] : 0.0f, hi, lo);
-    *reinterpret_cast<uint32_t*>(packed + (int64_t)place * 2 * RT + c) = hi;
-    *reinterpret_cast<uint32_t*>(packed + (int64_t)place * 2 * RT + RT + c) = lo;
-}
-
-// out[i, 0 .. ld) = in[i, 0 .. R) with zeros behind it: rows of a rank that is no multiple of 8.
-__global__ void __launch_bounds__(kThreads) widen_kernel(const bf16* __restrict__ in, bf16* __restrict__ out, int64_t rows, int R,
-                                                         int ld) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= rows * ld) return;
-    const int64_t row = i / ld;
-    const int r = (int)(i % ld);
-    out[i] = r < R ? in[row * R + r] : __float2bfloat16_rn(0.0f);
-}
-
 // ---- update ----------------------------------------------------------------------------------
 
-// A CTA takes 128 rows of one adapter x kCols columns. T's columns lie in shared memory as [column][RT]
-// in padded rows, ordered so that a thread's four n-tiles give it eight consecutive columns: it
-// reads and writes `in` and `out` in 16-byte vectors straight from its accumulators, 64 bytes of a
-// row by each four lanes. P's parts are the MMAs' A operand and stay in registers.
+// A CTA takes 128 rows of one adapter and a run of 64-column stages. A stage is in's [128][64] box in
+// 128-byte rows (the two 64-byte halves of odd rows exchanged: a thread's 16-byte reads are then free of
+// bank conflicts) and T's 64 rows of [C, ld], padded. Warp w owns rows 16 w .. 16 w + 15: P's parts are the A
+// operand and stay in registers. Within each 32 columns T's rows are laid down so that a thread's four
+// n-tiles are eight consecutive columns: it reads 16 bytes of the box, which become the MMAs' initial
+// accumulators, and writes 16 bytes to `out`, four lanes 64 bytes of a row. The ring keeps three boxes
+// a CTA in flight. Beside the streams the kernel has issue slots to spare only if a stage costs few
+// instructions: addresses advance by one stride, ring slots are unrolled, nothing is staged twice.
 template <int RT>
-constexpr int update_cols() { return RT <= 32 ? 512 : 256; }
-template <int RT>
-constexpr int update_smem() { return update_cols<RT>() * (RT * 2 + 16); }
+struct UpdateShape {
+    static constexpr int box = kTile * 128;
+    static constexpr int t_pitch = RT * 2 + 16;
+    static constexpr int stage = box + 64 * t_pitch;
+    static constexpr int stages = 4;
+    static constexpr int smem = stages * stage + 128;
+};
+
+struct Update {
+    const bf16* packed;
+    const bf16* table;   // [count, C, ld]
+    const bf16* in;      // null: 0
+    bf16* out;           // may be `in`
+    int C, ld, splits;
+};
 
 template <int RT>
-__global__ void __launch_bounds__(kThreads, RT <= 32 ? 3 : 2) update_kernel(const bf16* __restrict__ packed,
-                                                                            const bf16* __restrict__ table, int64_t tstride,
-                                                                            int cs, int rs, PlanView plan, const bf16* in, bf16* out,
-                                                                            int M, int C, int R, int n) {
-    constexpr int kCols = update_cols<RT>(), kPitch = RT * 2 + 16;
-    extern __shared__ __align__(16) uint8_t raw[];
-    const Tile tile = tile_of(plan, blockIdx.y, M);
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int c0 = blockIdx.x * kCols;
-    // every CTA waits before it leaves, so that this grid never ends before the one before it
-    if (tile.rows <= 0 || tile.adapter >= n || (tile.adapter < 0 && in == out)) {
-        wait_for_previous();
-        return;
-    }
-    if (tile.adapter < 0) {      // rows without an adapter are copied
-        wait_for_previous();
-        for (int i = tid; i < tile.rows * (kCols / 8); i += kThreads) {
-            const int m = row_at(plan, tile.first + i / (kCols / 8), M), c = c0 + (i % (kCols / 8)) * 8;
-            if (m < 0 || c >= C || !SS1_SPAN_IN((int64_t)m * C + c, 8, (int64_t)M * C, kSiteAdaY)) continue;
-            const int64_t at = (int64_t)m * C + c;
-            *reinterpret_cast<uint4*>(out + at) = in ? *reinterpret_cast<const uint4*>(in + at) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void update_role(const Update& d, const PlanView& plan, const Tile& tile, int split, uint8_t* raw, int M,
+                                            int R, int n, bool table_is_new) {
+    using S = UpdateShape<RT>;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, C = d.C;
+    const int chunks = (C + 63) / 64, per = (chunks + d.splits - 1) / d.splits;
+    const int from = min(chunks, split * per), to = min(chunks, from + per);
+    [[maybe_unused]] const int64_t total = (int64_t)M * C, tsize = (int64_t)n * C * d.ld;
+    if (tile.rows <= 0 || tile.adapter >= n || from >= to || (tile.adapter < 0 && d.in == d.out)) return;
+    if (tile.adapter < 0) {      // rows without an adapter are copied: a row a warp, eight vectors of a lane in flight
+        constexpr int kFlight = 8;
+        const int c1 = min(C, to * 64);
+        for (int r = warp; r < tile.rows; r += kThreads / 32) {
+            const int m = row_at(plan, tile.first + r, M);
+            if (m < 0) continue;
+            for (int c = from * 64 + lane * 8; c < c1; c += 32 * 8 * kFlight) {
+                uint4 v[kFlight];
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const int64_t at = (int64_t)m * C + c + i * 256;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (d.in && c + i * 256 < c1 && SS1_SPAN_IN(at, 8, total, kSiteAdaY)) v[i] = *reinterpret_cast<const uint4*>(d.in + at);
+                }
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const int64_t at = (int64_t)m * C + c + i * 256;
+                    if (c + i * 256 < c1 && SS1_SPAN_IN(at, 8, total, kSiteAdaY)) *reinterpret_cast<uint4*>(d.out + at) = v[i];
+                }
+            }
         }
         return;
     }
-    // shared-memory row of column n: within each 32, column 8 t + 2 j + b is row 8 j + 2 t + b
-    const bf16* T = table + (int64_t)tile.adapter * tstride;
-    const int cols = min(kCols, C - c0);
-    auto slot = [](int c) { return (c & ~31) | ((c & 6) << 2) | ((c & 24) >> 2) | (c & 1); };
-    if (rs == 1 && R % 8 == 0 && cs % 8 == 0) {      // T_a rows of R: 16-byte pieces
-        for (int i = tid; i < kCols * (RT / 8); i += kThreads) {
-            const int c = i / (RT / 8), r = (i % (RT / 8)) * 8;
-            const bool ok = c < cols && r < R && SS1_SPAN_IN(T + (int64_t)(c0 + c) * cs + r - table, 8, n * tstride, kSiteAdaB);
-            *reinterpret_cast<uint4*>(raw + slot(c) * kPitch + r * 2) =
-                ok ? *reinterpret_cast<const uint4*>(T + (int64_t)(c0 + c) * cs + r) : make_uint4(0, 0, 0, 0);
-        }
-    } else {                                         // transposed, or odd ranks: consecutive threads along the contiguous side
-        for (int i = tid; i < kCols * RT; i += kThreads) {
-            const int c = rs == 1 ? i / RT : i % kCols, r = rs == 1 ? i % RT : i / kCols;
-            const bool ok = c < cols && r < R && SS1_IN(T + (int64_t)(c0 + c) * cs + (int64_t)r * rs - table, n * tstride, kSiteAdaA);
-            *reinterpret_cast<bf16*>(raw + slot(c) * kPitch + r * 2) =
-                ok ? T[(int64_t)(c0 + c) * cs + (int64_t)r * rs] : __float2bfloat16_rn(0.0f);
-        }
+    const uint32_t base = (ptx::smem_u32(raw) + 127u) & ~127u;
+    uint8_t* const ring = raw + (base - ptx::smem_u32(raw));
+    const int uc = tid % 8;
+    const bf16* ip[4];           // this thread's pieces of a stage: a 16-byte chunk of four rows
+    bool iok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = tid / 8 + 32 * i;
+        const int m = r < tile.rows ? row_at(plan, tile.first + r, M) : -1;
+        iok[i] = m >= 0 && d.in;
+        ip[i] = (d.in ? d.in : d.table) + (iok[i] ? (int64_t)m * C + from * 64 + uc * 8 : 0);
     }
+    constexpr int kPieces = 64 * (RT / 8), kMine = (kPieces + kThreads - 1) / kThreads;
+    const bf16* tp[kMine];
+    bool tok[kMine];
+    uint32_t tdst[kMine];
+    int tcol[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int k = tid + i * kThreads, c = k / (RT / 8), r = (k % (RT / 8)) * 8;
+        tok[i] = k < kPieces && r < d.ld;
+        tcol[i] = from * 64 + c;
+        tp[i] = d.table + (tok[i] ? ((int64_t)tile.adapter * C + tcol[i]) * d.ld + r : 0);
+        // column 8 t + 2 j + b of each 32 is row 8 j + 2 t + b
+        tdst[i] = S::box + ((c & 32) | ((c & 6) << 2) | ((c & 24) >> 2) | (c & 1)) * S::t_pitch + r * 2;
+    }
+    int icol = from * 64 + uc * 8;
+    auto load = [&](bool some, int slot) {      // the next stage in line
+        if (some) {
+            const uint32_t su = base + slot * S::stage;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = tid / 8 + 32 * i;
+                const bool ok = iok[i] && icol < C && SS1_SPAN_IN(ip[i] - d.in, 8, total, kSiteAdaY);
+                copy16(su + r * 128 + ((uc ^ ((r & 1) << 2)) << 4), ok ? ip[i] : d.table, ok);
+                ip[i] += 64;
+            }
+            icol += 64;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const bool ok = tok[i] && tcol[i] < C && SS1_SPAN_IN(tp[i] - d.table, 8, tsize, kSiteAdaB);
+                if (kPieces % kThreads == 0 || tid + i * kThreads < kPieces) copy16(su + tdst[i], ok ? tp[i] : d.table, ok);
+                tp[i] += (int64_t)64 * d.ld;
+                tcol[i] += 64;
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    if (table_is_new) wait_for_previous();
+#pragma unroll
+    for (int s = 0; s < S::stages - 1; ++s) load(from + s < to, s);
     const int g = lane / 4, t4 = lane % 4;
-    const int r0 = warp * 16 + g;
-    const int m0 = r0 < tile.rows ? row_at(plan, tile.first + r0, M) : -1;
-    const int m1 = r0 + 8 < tile.rows ? row_at(plan, tile.first + r0 + 8, M) : -1;
-    __syncthreads();
-    wait_for_previous();
-    if (warp * 16 >= tile.rows) return;
+    bf16* op[2];                 // the two rows that this thread writes
+    bool ook[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = warp * 16 + g + 8 * h;
+        const int m = r < tile.rows ? row_at(plan, tile.first + r, M) : -1;
+        ook[h] = m >= 0;
+        op[h] = d.out + (m >= 0 ? (int64_t)m * C : 0) + from * 64 + t4 * 8;
+    }
+    wait_for_previous();         // `packed` is the previous kernel's; `in` and `out` are not its
     uint32_t hi[RT / 16][4], lo[RT / 16][4];
     {
-        const int last = tile.first + tile.rows - 1;   // rows behind the tile's end read its last one; they are not written
-        const uint32_t* p0 = reinterpret_cast<const uint32_t*>(packed + (int64_t)min(tile.first + r0, last) * 2 * RT);
-        const uint32_t* p1 = reinterpret_cast<const uint32_t*>(packed + (int64_t)min(tile.first + r0 + 8, last) * 2 * RT);
+        const int last = tile.first + tile.rows - 1, r0 = tile.first + warp * 16 + g;   // rows behind the end read the last one
+        const uint32_t* p0 = reinterpret_cast<const uint32_t*>(d.packed + (int64_t)min(r0, last) * 2 * RT);
+        const uint32_t* p1 = reinterpret_cast<const uint32_t*>(d.packed + (int64_t)min(r0 + 8, last) * 2 * RT);
 #pragma unroll
         for (int k = 0; k < RT / 16; ++k) {
             hi[k][0] = p0[k * 8 + t4];
@@ -344,75 +460,85 @@ __global__ void __launch_bounds__(kThreads, RT <= 32 ? 3 : 2) update_kernel(cons
             lo[k][3] = p1[RT / 2 + k * 8 + 4 + t4];
         }
     }
-    const uint32_t base = ptx::smem_u32(raw);
-    constexpr int kBatch = 4;      // 32-column steps whose vectors are in flight together
-    for (int q0 = 0; q0 * 32 < cols; q0 += kBatch) {
-        uint4 y[kBatch][2];
+    const bool busy = warp * 16 < tile.rows;
+    const uint32_t frag = (lane / 16 * 8 + lane % 8) * S::t_pitch + (lane / 8 % 2) * 16;   // this lane's row of T's fragments
+    int ocol = from * 64 + t4 * 8;
+    for (int first = from; first < to; first += S::stages)
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int c = c0 + (q0 + q) * 32 + t4 * 8;
-            y[q][0] = y[q][1] = make_uint4(0, 0, 0, 0);
-            if (in && c < C) {
-                if (m0 >= 0 && SS1_SPAN_IN((int64_t)m0 * C + c, 8, (int64_t)M * C, kSiteAdaY))
-                    y[q][0] = *reinterpret_cast<const uint4*>(in + (int64_t)m0 * C + c);
-                if (m1 >= 0 && SS1_SPAN_IN((int64_t)m1 * C + c, 8, (int64_t)M * C, kSiteAdaY))
-                    y[q][1] = *reinterpret_cast<const uint4*>(in + (int64_t)m1 * C + c);
-            }
-        }
+        for (int s = 0; s < S::stages; ++s) {
+            if (first + s >= to) break;
+            ptx::cp_async_wait<S::stages - 2>();
+            __syncthreads();
+            load(first + s + S::stages - 1 < to, (s + S::stages - 1) % S::stages);
+            if (!busy) continue;
+            const uint32_t stt = base + s * S::stage + S::box + frag;
+            const uint8_t* box = ring + s * S::stage + (warp * 16 + g) * 128;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            if ((q0 + q) * 32 >= cols) break;
-            float acc[4][4];
+            for (int half = 0; half < 2; ++half) {
+                float acc[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int h = 0; h < 2; ++h) {     // rows g and g + 8 have the same parity
+                    const uint4 y = *reinterpret_cast<const uint4*>(box + h * 8 * 128 + (((half * 4 + t4) ^ ((g & 1) << 2)) << 4));
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < RT / 16; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    uint32_t b[4];
-                    ldsm4(b, base + ((q0 + q) * 32 + (j + lane / 16) * 8 + lane % 8) * kPitch + (k * 2 + (lane / 8) % 2) * 16);
-                    mma16816(acc[j], lo[k], b[0], b[1]);
-                    mma16816(acc[j], hi[k], b[0], b[1]);
-                    mma16816(acc[j + 1], lo[k], b[2], b[3]);
-                    mma16816(acc[j + 1], hi[k], b[2], b[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        acc[j][2 * h] = __uint_as_float(w[j] << 16);
+                        acc[j][2 * h + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                    }
                 }
-            const int c = c0 + (q0 + q) * 32 + t4 * 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int m = h ? m1 : m0;
-                if (m < 0 || c >= C) continue;
-                Raw8<bf16> v;
-                v.a = y[q][h];
-                float f[8];
-                v.get(f);
+                for (int k = 0; k < RT / 16; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[2 * j] += acc[j][2 * h];
-                    f[2 * j + 1] += acc[j][2 * h + 1];
+                    for (int j = 0; j < 4; j += 2) {
+                        uint32_t b[4];
+                        ldsm4(b, stt + (half * 32 + j * 8) * S::t_pitch + k * 32);
+                        mma16816(acc[j], lo[k], b[0], b[1]);
+                        mma16816(acc[j + 1], lo[k], b[2], b[3]);
+                        mma16816(acc[j], hi[k], b[0], b[1]);
+                        mma16816(acc[j + 1], hi[k], b[2], b[3]);
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[j][2 * h], acc[j][2 * h + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    if (ook[h] && ocol + half * 32 < C && SS1_SPAN_IN(op[h] + half * 32 - d.out, 8, total, kSiteAdaY))
+                        *reinterpret_cast<uint4*>(op[h] + half * 32) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                v.set(f);
-                if (SS1_SPAN_IN((int64_t)m * C + c, 8, (int64_t)M * C, kSiteAdaY)) v.store(out + (int64_t)m * C + c);
             }
+            op[0] += 64;
+            op[1] += 64;
+            ocol += 64;
         }
-    }
+    ptx::cp_async_wait<0>();
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, PlanView plan, int M, int R, int n) {
+    extern __shared__ uint8_t raw[];
+    update_role<RT>(d, plan, tile_of(plan, blockIdx.y, M), blockIdx.x, raw, M, R, n, false);
+    wait_for_previous();   // also in CTAs that left early: this grid never ends before the one before it
 }
 
 // ---- columns ---------------------------------------------------------------------------------
 
-// A CTA takes 256 columns of one adapter and a share of its rows, 64 rows a stage: U as four
-// [64][64] boxes in swizzled 128-byte rows, P's packed rows in padded ones. Warp w owns columns
-// 32 w .. 32 w + 31: U transposed out of shared memory is the A operand (column x row), P the B
-// operand, and the sums over all rows stay in registers.
-constexpr int kColCols = 256, kColRows = 64;
+// A CTA takes 256 columns and a run of tiles, 32 rows a stage: U as four [32][64] boxes in swizzled
+// 128-byte rows, P's packed rows in padded ones. Warp w owns columns 32 w .. 32 w + 31: U transposed
+// out of shared memory is the A operand (column x row), P the B operand, and the sums stay in registers
+// until the run comes to another adapter. The tiles are dealt evenly whatever their adapters: run k's sums
+// for adapter a go to part[k + a] (k and a only grow along the list, so no two share a place), or
+// straight to `out` where the run has all of the adapter's tiles.
+constexpr int kColCols = 256, kColRows = 32, kColSteps = kTile / kColRows;
 
 template <int RT>
 struct ColumnsShape {
     static constexpr int u_bytes = kColRows * kColCols * 2;
     static constexpr int p_pitch = RT * 4 + 16;
     static constexpr int stage = u_bytes + kColRows * p_pitch;
-    static constexpr int stages = RT <= 64 ? 4 : 3;
+    static constexpr int stages = RT <= 32 ? 5 : (RT <= 64 ? 4 : 3);
     static constexpr int smem = stages * stage + 128;
 };
 
@@ -420,39 +546,75 @@ struct Columns {
     const bf16* U;
     const bf16* packed;
     bf16* out;
-    float* part;        // partial sums of the shares, or null: one share, which writes `out`
-    int C, cs, rs, shares;
+    float* part;
+    int C, cs, rs, runs;
 };
 
+// Adapter a's tiles, and the tiles of a run.
+__device__ __forceinline__ int2 adapter_tiles(const PlanView& plan, int a, int M) {
+    if (plan.rows == nullptr) return make_int2(0, (M + kTile - 1) / kTile);
+    const int lo = min(max(plan.first_tile[a], 0), plan.max_tiles);
+    return make_int2(lo, min(max(plan.first_tile[a + 1], lo), plan.max_tiles));
+}
+__device__ __forceinline__ int tiles_a_run(const PlanView& plan, int n, int M, int runs) {
+    const int tiles = plan.rows == nullptr ? (M + kTile - 1) / kTile : min(max(plan.first_tile[n], 0), plan.max_tiles);
+    return max(1, (tiles + runs - 1) / runs);
+}
+
 template <int RT>
-__global__ void __launch_bounds__(kThreads) columns_kernel(const Columns d, PlanView plan, int M, int R, int n) {
+__device__ __forceinline__ void columns_role(const Columns& d, const PlanView& plan, int range, int run, uint8_t* raw, int M, int R,
+                                             int n) {
     using S = ColumnsShape<RT>;
-    extern __shared__ uint8_t raw[];
-    wait_for_previous();
     const uint32_t base = (ptx::smem_u32(raw) + 127u) & ~127u;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int a = blockIdx.y, share = blockIdx.z, C = d.C;
-    const int c0 = blockIdx.x * kColCols;
-    const int begin = plan.rows ? max(0, plan.first[a]) : 0, end = plan.rows ? min(M, plan.first[a + 1]) : M;
-    const int steps = end > begin ? (end - begin + kColRows - 1) / kColRows : 0, per = (steps + d.shares - 1) / d.shares;
-    const int from = min(steps, share * per), to = min(steps, from + per);
+    const int C = d.C, c0 = range * kColCols;
+    const int tiles = adapter_tiles(plan, n - 1, M).y, per = tiles_a_run(plan, n, M, d.runs);
+    const int t0 = min(tiles, run * per), t1 = min(tiles, t0 + per);
+    const int steps = (t1 - t0) * kColSteps;
+    static_assert(4 * kColSteps <= 32 && kColRows == 4 * (kThreads / 32), "a lane for each row of a warp's share of a tile");
 
-    auto load = [&](int step, int slot) {
-        if (step < to) {
-            const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
-            const int r0 = begin + step * kColRows;
+    // loads: a warp brings 512 bytes of each of its four rows of a stage. Lane 4 k + i looks up row i of the
+    // tile's stage k; rows are looked up a tile ahead, tiles two ahead, so that no load waits for a look-up.
+    const int lc = c0 + lane * 8;
+    const bool cok = lc < C;
+    uint32_t udst[4];
 #pragma unroll
-            for (int i = 0; i < kColRows * kColCols / 8 / kThreads; ++i) {
-                const int r = warp + i * 8, c = c0 + lane * 8;       // a warp brings 512 bytes of one row
-                const int m = r0 + r < end ? row_at(plan, r0 + r, M) : -1;
-                const bool ok = m >= 0 && c < C && SS1_SPAN_IN((int64_t)m * C + c, 8, (int64_t)M * C, kSiteAdaX);
-                copy16(su + (lane / 8) * (kColRows * 128) + r * 128 + (((lane % 8) ^ (r & 7)) << 4), ok ? d.U + (int64_t)m * C + c : d.U,
-                       ok);
+    for (int i = 0; i < 4; ++i) {
+        const int r = warp * 4 + i;
+        udst[i] = (lane / 8) * (kColRows * 128) + r * 128 + (((lane % 8) ^ (r & 7)) << 4);
+    }
+    constexpr int kPieces = kColRows * (RT / 4), kMine = (kPieces + kThreads - 1) / kThreads;
+    auto tile_at = [&](int t) { return t < t1 ? tile_of(plan, t, M) : Tile{-1, 0, 0}; };
+    auto row_of = [&](const Tile& t) {
+        const int r = (lane / 4) * kColRows + warp * 4 + lane % 4;
+        return lane < 4 * kColSteps && r < t.rows ? row_at(plan, t.first + r, M) : -1;
+    };
+    Tile now = tile_at(t0), next = tile_at(t0 + 1), after = tile_at(t0 + 2);   // of the stage to be loaded
+    int now_row = row_of(now), next_row = row_of(next);
+    auto load = [&](int step, int slot) {
+        if (step < steps) {
+            const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
+            const int k = step % kColSteps;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = __shfl_sync(0xFFFFFFFFu, now_row, k * 4 + i);
+                const int64_t at = (int64_t)m * C + lc;
+                const bool ok = m >= 0 && cok && SS1_SPAN_IN(at, 8, (int64_t)M * C, kSiteAdaX);
+                copy16(su + udst[i], ok ? d.U + at : d.U, ok);
             }
-            for (int i = tid; i < kColRows * (RT / 4); i += kThreads) {
-                const int r = i / (RT / 4), c = (i % (RT / 4)) * 8;
-                const bool ok = r0 + r < end && SS1_SPAN_IN((int64_t)(r0 + r) * 2 * RT + c, 8, (int64_t)M * 2 * RT, kSiteAdaG);
-                copy16(sp + r * S::p_pitch + c * 2, ok ? d.packed + (int64_t)(r0 + r) * 2 * RT + c : d.packed, ok);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int e = tid + i * kThreads, r = e / (RT / 4), c = (e % (RT / 4)) * 8;
+                const int64_t at = (int64_t)(now.first + k * kColRows + r) * 2 * RT + c;
+                const bool ok = k * kColRows + r < now.rows && SS1_SPAN_IN(at, 8, (int64_t)M * 2 * RT, kSiteAdaG);
+                if (kPieces % kThreads == 0 || e < kPieces) copy16(sp + r * S::p_pitch + c * 2, ok ? d.packed + at : d.packed, ok);
+            }
+            if (k == kColSteps - 1) {
+                now = next;
+                now_row = next_row;
+                next = after;
+                next_row = row_of(next);
+                after = tile_at(t0 + step / kColSteps + 3);
             }
         }
         ptx::cp_async_commit();
@@ -465,14 +627,43 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Columns d, Plan
         for (int j = 0; j < RT / 8; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[h][j][i] = 0.0f;
-    for (int s = 0; s < S::stages - 1; ++s) load(from + s, s);
+    int adapter = now.adapter, next_adapter = adapter;
+    for (int s = 0; s < S::stages - 1; ++s) load(s, s);
     const bool busy = c0 + warp * 32 < C;
-    for (int step = from; step < to; ++step) {
+    const int64_t size = (int64_t)C * R;
+    for (int step = 0, slot = 0;; ++step) {
+        if (step % kColSteps == 0 || step == steps) {       // a tile begins, or the run ends
+            const int a = step < steps ? next_adapter : -1;
+            if (step + kColSteps < steps) next_adapter = tile_of(plan, t0 + step / kColSteps + 1, M).adapter;
+            if (a != adapter && busy && (unsigned)adapter < (unsigned)n) {
+                const int2 own = adapter_tiles(plan, adapter, M);
+                const bool whole = own.x >= t0 && own.y <= t1;
+                const int64_t place = whole ? adapter * size : (int64_t)(run + adapter) * size;
+                [[maybe_unused]] const int64_t all = (whole ? n : d.runs + n) * size;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = c0 + warp * 32 + h * 16 + lane / 4 + (i / 2) * 8, r = j * 8 + (lane % 4) * 2 + i % 2;
+                            const int64_t at = place + (int64_t)c * d.cs + (int64_t)r * d.rs;
+                            if (c < C && r < R && SS1_IN(at, all, kSiteAdaPart)) {
+                                if (whole) d.out[at] = __float2bfloat16_rn(acc[h][j][i]);
+                                else d.part[at] = acc[h][j][i];
+                            }
+                            acc[h][j][i] = 0.0f;
+                        }
+            }
+            adapter = a;
+            if (step == steps) break;
+        }
         ptx::cp_async_wait<S::stages - 2>();
         __syncthreads();
-        load(step + S::stages - 1, (step - from + S::stages - 1) % S::stages);
+        load(step + S::stages - 1, slot == 0 ? S::stages - 1 : slot - 1);
+        const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
+        slot = slot == S::stages - 1 ? 0 : slot + 1;
         if (!busy) continue;
-        const uint32_t su = base + ((step - from) % S::stages) * S::stage, sp = su + S::u_bytes;
         const int mat = lane / 8, l8 = lane % 8;
 #pragma unroll
         for (int k = 0; k < kColRows / 16; ++k) {
@@ -491,172 +682,197 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Columns d, Plan
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     mma16816(acc[h][j], u[h], l[0], l[1]);
-                    mma16816(acc[h][j], u[h], b[0], b[1]);
                     mma16816(acc[h][j + 1], u[h], l[2], l[3]);
+                    mma16816(acc[h][j], u[h], b[0], b[1]);
                     mma16816(acc[h][j + 1], u[h], b[2], b[3]);
                 }
             }
         }
     }
     ptx::cp_async_wait<0>();
-    if (!busy) return;
-    const int64_t size = (int64_t)n * C * R;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = c0 + warp * 32 + h * 16 + lane / 4 + (i / 2) * 8, r = j * 8 + (lane % 4) * 2 + i % 2;
-                if (c >= C || r >= R) continue;
-                const int64_t at = (int64_t)a * C * R + (int64_t)c * d.cs + (int64_t)r * d.rs;
-                if (!SS1_IN(at, size, kSiteAdaPart)) continue;
-                if (d.part) d.part[share * size + at] = acc[h][j][i];
-                else d.out[at] = __float2bfloat16_rn(acc[h][j][i]);
-            }
 }
 
-// out[i] = the shares' partial sums, in share order, for both gradients (y = 0, 1).
+// dB, dA and dX in one launch: each needs only G and what prepare_kernel wrote, and their streams overlap.
+// CTAs 0 .. nb - 1 take dB (dY, just read for G, is partly still in L2), then na take dA, the rest dX.
+template <int RT>
+constexpr int gradients_smem() {
+    return ColumnsShape<RT>::smem > UpdateShape<RT>::smem ? ColumnsShape<RT>::smem : UpdateShape<RT>::smem;
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) gradients_kernel(const Columns db, int nb, const Columns da, int na,
+                                                                               const Update dx, PlanView plan, int M, int R, int n) {
+    extern __shared__ uint8_t raw[];
+    let_next_start();
+    wait_for_previous();
+    const int i = blockIdx.x;
+    if (i < nb + na) {
+        const bool b = i < nb;
+        const Columns& d = b ? db : da;
+        const int ranges = (d.C + kColCols - 1) / kColCols, k = b ? i : i - nb;
+        columns_role<RT>(d, plan, k % ranges, k / ranges, raw, M, R, n);
+    } else {
+        const int k = i - nb - na;
+        update_role<RT>(dx, plan, tile_of(plan, k / dx.splits, M), k % dx.splits, raw, M, R, n, true);
+    }
+}
+
+// The runs' partial sums, in run order, for the adapters whose tiles lie in several runs; zeros for those
+// without rows. y = 0: dA, 1: dB; z: adapters.
 struct Sums {
     const float* part[2];
     bf16* out[2];
-    int64_t size[2];
-    int shares[2];
+    int64_t size[2];         // elements of one adapter
+    int runs[2];
 };
-__global__ void __launch_bounds__(kThreads) add_kernel(const Sums s) {
+__global__ void __launch_bounds__(kThreads) add_kernel(const Sums s, PlanView plan, int M, int n) {
     wait_for_previous();
     const int w = blockIdx.y;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (s.part[w] == nullptr || i >= s.size[w]) return;
-    float v = 0.0f;
-    for (int k = 0; k < s.shares[w]; ++k) v += s.part[w][k * s.size[w] + i];
-    s.out[w][i] = __float2bfloat16_rn(v);
+    if (s.out[w] == nullptr) return;
+    const int64_t size = s.size[w];
+    const int per = tiles_a_run(plan, n, M, s.runs[w]);
+    for (int a = blockIdx.z; a < n; a += gridDim.z) {
+        const int2 own = adapter_tiles(plan, a, M);
+        const int lo = own.x / per, hi = own.y > own.x ? min((own.y - 1) / per, s.runs[w] - 1) : lo - 1;
+        if (lo == hi) continue;          // written by the run itself
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += (int64_t)gridDim.x * kThreads) {
+            float v = 0.0f;
+            for (int k = lo; k <= hi; ++k) v += s.part[w][(int64_t)(k + a) * size + i];
+            s.out[w][a * size + i] = __float2bfloat16_rn(v);
+        }
+    }
 }
 
 // ---- launches --------------------------------------------------------------------------------
 
 int tiles_at_most(const Call& c) { return c.plan.rows ? c.plan.max_tiles : (int)((c.M + kTile - 1) / kTile); }
 
+// Shares of the columns for `tiles` row tiles: about `ctas` CTAs in all, at least four 64-column stages each.
+int stage_splits(int64_t C, int tiles, int ctas) {
+    const int most = (int)((C + 255) / 256);
+    int s = ctas / tiles;
+    s = s > most ? most : s;
+    return s < 1 ? 1 : s;
+}
+
+// H packed and A transposed where the pointers are given, B widened where R is no multiple of 8; *B and *ld: B as
+// the kernels read it.
+template <int RT>
+cudaError_t prepare(const Call& c, const MmaSpace& w, const float* H, bool turn_a, bool with_b, const void** B, int* ld,
+                    cudaStream_t st) {
+    Prepare d = {};
+    d.ld = (c.R + 7) / 8 * 8;
+    *ld = d.ld;
+    *B = c.B;
+    auto ctas = [](int64_t work) { return (int)(work > 592 ? 592 : work); };
+    if (H) {
+        d.H = H; d.index = c.index; d.scale = c.scale; d.packed_h = (bf16*)w.packed_h;
+        d.nh = ctas((c.M * (RT / 2) + kThreads - 1) / kThreads);
+    }
+    if (with_b && c.R % 8) {
+        d.B = (const bf16*)c.B; d.wide_b = (bf16*)w.wide_b; d.b_rows = (int64_t)c.n * c.N;
+        d.nb = ctas((d.b_rows * d.ld + kThreads - 1) / kThreads);
+        *B = w.wide_b;
+    }
+    if (turn_a) {
+        d.A = (const bf16*)c.A; d.turned_a = (bf16*)w.turned_a; d.K = (int)c.K;
+        d.na = ctas((c.K + 31) / 32 * ((d.ld + 31) / 32) * c.n);
+    }
+    if (d.nh + d.nb + d.na == 0) return cudaSuccess;
+    prepare_kernel<RT><<<(unsigned)(d.nh + d.nb + d.na), kThreads, 0, st>>>(d, c.plan, (int)c.M, c.R, c.n);
+    return cudaGetLastError();
+}
+
 template <int RT, bool TRANS>
-cudaError_t products(const Call& c, const void* U, const void* table, int ld, int64_t C, float* H, void* packed,
-                     bool scale_packed, cudaStream_t st) {
+cudaError_t products(const Call& c, const void* U, const void* table, int ld, int64_t C, float* H, void* packed, cudaStream_t st) {
     using S = ProductsShape<RT, TRANS>;
     auto* fn = &products_kernel<RT, TRANS>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
     if (e != cudaSuccess) return e;
     const int tiles = tiles_at_most(c);
-    // two CTAs for each of 148 SMs, at least four stages of columns each, clusters of a portable size
-    int splits = 296 / tiles;
-    const int most = (int)((C + 255) / 256);
-    splits = splits > most ? most : splits;
-    splits = splits < 1 ? 1 : (splits > 8 ? 8 : splits);
+    int splits = stage_splits(C, tiles, 296);
+    splits = splits > 8 ? 8 : splits;                 // clusters of a portable size
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)splits, (unsigned)tiles);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)splits;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, (const bf16*)U, (const bf16*)table, ld, c.scale, c.plan, H, (bf16*)packed, scale_packed,
-                              (int)c.M, (int)C, c.R, c.n);
+    cfg.numAttrs = TRANS ? 2 : 1;                     // backward: after prepare_kernel
+    return cudaLaunchKernelEx(&cfg, fn, (const bf16*)U, (const bf16*)table, ld, c.scale, c.plan, H, (bf16*)packed, (int)c.M, (int)C, c.R,
+                              c.n);
 }
 
 template <int RT>
-cudaError_t update(const Call& c, const void* packed, const void* table, int64_t C, int cs, int rs, const void* in, void* out,
-                   cudaStream_t st) {
+cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st) {
+    int ld;
+    const void* B;
+    cudaError_t e = prepare<RT>(c, w, nullptr, false, true, &B, &ld, st);
+    if (e == cudaSuccess) e = products<RT, false>(c, X, c.A, c.R, c.K, H, w.packed_g, st);
+    using S = UpdateShape<RT>;
     auto* fn = &update_kernel<RT>;
-    const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), update_smem<RT>());
+    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((C + update_cols<RT>() - 1) / update_cols<RT>()), (unsigned)tiles_at_most(c));
-    return launch_dependent(fn, grid, dim3(kThreads), update_smem<RT>(), st, (const bf16*)packed, (const bf16*)table,
-                            (int64_t)C * c.R, cs, rs, c.plan, (const bf16*)in, (bf16*)out, (int)c.M, (int)C, c.R, c.n);
-}
-
-template <int RT>
-cudaError_t columns(const Call& c, const Columns& d, cudaStream_t st) {
-    using S = ColumnsShape<RT>;
-    auto* fn = &columns_kernel<RT>;
-    const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((d.C + kColCols - 1) / kColCols), (unsigned)c.n, (unsigned)d.shares);
-    return launch_dependent(fn, grid, dim3(kThreads), S::smem, st, d, c.plan, (int)c.M, c.R, c.n);
-}
-
-template <int RT>
-cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, float* H, void* packed, cudaStream_t st) {
-    const cudaError_t e = products<RT, false>(c, X, c.A, c.R, c.K, H, packed, true, st);
-    if (e != cudaSuccess) return e;
-    return update<RT>(c, packed, c.B, c.N, c.R, 1, Y, out, st);
+    const int tiles = tiles_at_most(c), splits = stage_splits(c.N, tiles, 296);
+    const Update d{(const bf16*)w.packed_g, (const bf16*)B, (const bf16*)Y, (bf16*)out, (int)c.N, ld, splits};
+    return launch_dependent(fn, dim3((unsigned)splits, (unsigned)tiles), dim3(kThreads), S::smem, st, d, c.plan, (int)c.M, c.R, c.n);
 }
 
 template <int RT>
 cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
                         const MmaSpace& w, cudaStream_t st) {
-    cudaError_t e = cudaSuccess;
-    if (dB) {
-        const int64_t pairs = c.M * (RT / 2);
-        pack_kernel<RT><<<(unsigned)((pairs + kThreads - 1) / kThreads), kThreads, 0, st>>>(H, c.index, c.scale, c.plan, (bf16*)w.packed_h,
-                                                                                          (int)c.M, c.R, c.n);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && (dX || dA)) {
-        const void* B = c.B;
-        int ld = c.R;
-        if (c.R % 8) {
-            ld = (c.R + 7) / 8 * 8;
-            const int64_t size = (int64_t)c.n * c.N * ld;
-            widen_kernel<<<(unsigned)((size + kThreads - 1) / kThreads), kThreads, 0, st>>>((const bf16*)c.B, (bf16*)w.wide_b,
-                                                                                           (int64_t)c.n * c.N, c.R, ld);
-            e = cudaGetLastError();
-            B = w.wide_b;
-        }
-        if (e == cudaSuccess) e = products<RT, true>(c, dY, B, ld, c.N, nullptr, w.packed_g, true, st);
-    }
+    int ld;
+    const void* B;
+    cudaError_t e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, st);
+    if (e == cudaSuccess && (dX || dA)) e = products<RT, true>(c, dY, B, ld, c.N, nullptr, w.packed_g, st);
+    auto* fn = &gradients_kernel<RT>;
+    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), gradients_smem<RT>());
+    if (e != cudaSuccess) return e;
+    const int rb = mma_runs(c.M, c.N, c.n), ra = mma_runs(c.M, c.K, c.n);
+    const Columns db{(const bf16*)dY, (const bf16*)w.packed_h, (bf16*)dB, w.part_b, (int)c.N, c.R, 1, rb};
+    const Columns da{(const bf16*)X, (const bf16*)w.packed_g, (bf16*)dA, w.part_a, (int)c.K, 1, (int)c.K, ra};
+    const int nb = dB ? (db.C + kColCols - 1) / kColCols * rb : 0;
+    const int na = dA ? (da.C + kColCols - 1) / kColCols * ra : 0;
+    const int tiles = tiles_at_most(c);
+    const Update dx{(const bf16*)w.packed_g, (const bf16*)w.turned_a, (const bf16*)dX_in, (bf16*)dX, (int)c.K, ld, stage_splits(c.K, tiles, 148)};
+    const int64_t ctas = (int64_t)nb + na + (dX ? (int64_t)tiles * dx.splits : 0);
+    e = launch_dependent(fn, dim3((unsigned)ctas), dim3(kThreads), gradients_smem<RT>(), st, db, nb, da, na, dx, c.plan, (int)c.M, c.R,
+                         c.n);
+    if (e != cudaSuccess || (!dA && !dB)) return e;
     Sums s = {};
-    if (e == cudaSuccess && dB) {
-        const int shares = mma_shares(c.M, c.N, c.n);
-        const Columns d{(const bf16*)dY, (const bf16*)w.packed_h, (bf16*)dB, shares > 1 ? w.part_b : nullptr, (int)c.N, c.R, 1, shares};
-        e = columns<RT>(c, d, st);
-        s.part[1] = d.part; s.out[1] = d.out; s.size[1] = (int64_t)c.n * c.N * c.R; s.shares[1] = shares;
-    }
-    if (e == cudaSuccess && dX) e = update<RT>(c, w.packed_g, c.A, c.K, 1, (int)c.K, dX_in, dX, st);
-    if (e == cudaSuccess && dA) {
-        const int shares = mma_shares(c.M, c.K, c.n);
-        const Columns d{(const bf16*)X, (const bf16*)w.packed_g, (bf16*)dA, shares > 1 ? w.part_a : nullptr, (int)c.K, 1, (int)c.K, shares};
-        e = columns<RT>(c, d, st);
-        s.part[0] = d.part; s.out[0] = d.out; s.size[0] = (int64_t)c.n * c.K * c.R; s.shares[0] = shares;
-    }
-    if (e == cudaSuccess && (s.part[0] || s.part[1])) {
-        const int64_t size = s.size[0] > s.size[1] ? s.size[0] : s.size[1];
-        e = launch_dependent(&add_kernel, dim3((unsigned)((size + kThreads - 1) / kThreads), 2), dim3(kThreads), 0, st, s);
-    }
-    return e;
+    if (dA) { s.part[0] = da.part; s.out[0] = da.out; s.size[0] = (int64_t)c.K * c.R; s.runs[0] = ra; }
+    if (dB) { s.part[1] = db.part; s.out[1] = db.out; s.size[1] = (int64_t)c.N * c.R; s.runs[1] = rb; }
+    const int64_t size = s.size[0] > s.size[1] ? s.size[0] : s.size[1], blocks = (size + kThreads - 1) / kThreads;
+    return launch_dependent(&add_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), 2, (unsigned)(c.n < 64 ? c.n : 64)),
+                            dim3(kThreads), 0, st, s, c.plan, (int)c.M, c.n);
 }
 
 }  // namespace
 
 int mma_rank(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
 
-int mma_shares(int64_t M, int64_t C, int n) {
-    // one CTA for each of 148 SMs, at least four stages of rows a share
-    const int64_t ctas = (C + kColCols - 1) / kColCols * n;
-    int64_t s = 148 / ctas;
-    const int64_t most = M / (4 * kColRows);
+int mma_runs(int64_t M, int64_t C, int n) {
+    // a quarter of two CTAs for each of 148 SMs (dB and dA each move half of dX's bytes), at least two
+    // tiles a run
+    int64_t s = 74 / ((C + kColCols - 1) / kColCols);
+    const int64_t most = (M / kTile + 1) / 2;
     s = s > most ? most : s;
-    return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
+    return (int)(s < 1 ? 1 : s);
 }
 
-cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, void* packed, cudaStream_t st) {
+cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st) {
     switch (mma_rank(c.R)) {
-        case 16: return forward_rt<16>(c, X, Y, out, H, packed, st);
-        case 32: return forward_rt<32>(c, X, Y, out, H, packed, st);
-        case 64: return forward_rt<64>(c, X, Y, out, H, packed, st);
-        default: return forward_rt<128>(c, X, Y, out, H, packed, st);
+        case 16: return forward_rt<16>(c, X, Y, out, H, w, st);
+        case 32: return forward_rt<32>(c, X, Y, out, H, w, st);
+        case 64: return forward_rt<64>(c, X, Y, out, H, w, st);
+        default: return forward_rt<128>(c, X, Y, out, H, w, st);
     }
 }
 

@@ -8,8 +8,10 @@ implementation. Tensors are contiguous CUDA tensors, bf16 or float32.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import struct
+from operator import attrgetter
 from typing import List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -33,8 +35,8 @@ def _tensor(name: str, t: torch.Tensor, shape=None, dtype=None, device=None) -> 
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, not {t.device}")
     return t
 
 
@@ -42,22 +44,25 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr() if t is not None else None
 
 
-class _On:
-    """The library call's device and stream: makes `device` current for the call where it is not, and
-    ties the tensors that this module allocated to a stream other than the one they came from."""
-
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.guard = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = stream
-        self.handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def made(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _call(device: int, stream: Optional[torch.cuda.Stream], made, fn, *args):
+    """fn(*args, stream handle) on `device` (made current for the call where it is not); on a stream other
+    than the one that they came from, `made` (tensors that this module allocated) are tied to it."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+        handle = stream.cuda_stream
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status, fn.__name__)
 
 
 def _apart(out: torch.Tensor, name: str, **inputs):
@@ -70,16 +75,32 @@ def _apart(out: torch.Tensor, name: str, **inputs):
 
 # ---- layer norm ------------------------------------------------------------------------------
 
-def _norm_weights(X: torch.Tensor, **weights) -> torch.dtype:
+def _norm_weights(X: torch.Tensor, device: int, weight, bias=None) -> torch.dtype:
+    """The weights' type; X's without weights."""
     dt = None
-    for name, w in weights.items():
+    for name, w in (("weight", weight), ("bias", bias)):
         if w is None:
             continue
-        _tensor(name, w, (X.shape[1],), device=X.device)
-        if w.dtype not in (X.dtype, torch.float32) or (dt is not None and w.dtype != dt):
+        _tensor(name, w, X.shape[1:], None, device)
+        t = w.dtype
+        if (t != X.dtype and t != torch.float32) or (dt is not None and t != dt):
             raise ValueError(f"{name} must have X's dtype or float32, and weight and bias one dtype")
-        dt = w.dtype
+        dt = t
     return dt if dt is not None else X.dtype
+
+
+def _norm_rows(X: torch.Tensor) -> Tuple[int, int]:
+    _tensor("X", X)
+    if X.dim() != 2 or X.shape[1] < 1:
+        raise ValueError("X must be [M, K] with K >= 1")
+    return X.shape
+
+
+@functools.lru_cache(maxsize=None)
+def _norm_workspace(L, M: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(L.ss1_layernorm_backward_workspace(M, K, ctypes.byref(n)), "ss1_layernorm_backward_workspace")
+    return n.value
 
 
 def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -87,25 +108,17 @@ def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bi
                       stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(Y, mean, rstd) of X [M, K]: Y in X's dtype, mean and rstd float32 [M] (ss1_layernorm_forward).
     weight and bias [K] in X's dtype, or float32 beside bf16 rows."""
-    _tensor("X", X)
-    if X.dim() != 2 or X.shape[1] < 1:
-        raise ValueError("X must be [M, K] with K >= 1")
-    wt = _norm_weights(X, weight=weight, bias=bias)
-    M, K = X.shape
-    on = _On(X.device, stream)
+    M, K = _norm_rows(X)
+    device = X.get_device()
+    wt = _norm_weights(X, device, weight, bias)
     if out is None:
         Y = torch.empty_like(X)
-        on.made(Y)
     else:
-        Y = _tensor("out", out, X.shape, X.dtype, X.device)
+        Y = _tensor("out", out, X.shape, X.dtype, device)
         _apart(Y, "out", X=X, weight=weight, bias=bias)
-    stats = torch.empty((2, M), dtype=torch.float32, device=X.device)
-    on.made(stats)
-    mean, rstd = stats.unbind(0)
-    with on.guard:
-        _check(lib().ss1_layernorm_forward(X.data_ptr(), _ptr(weight), _ptr(bias), Y.data_ptr(), mean.data_ptr(),
-                                           rstd.data_ptr(), M, K, eps, _dtype_code(X.dtype), _dtype_code(wt), on.handle),
-               "ss1_layernorm_forward")
+    mean, rstd = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
+    _call(device, stream, (Y if out is None else None, mean, rstd), lib().ss1_layernorm_forward, X.data_ptr(), _ptr(weight),
+          _ptr(bias), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), M, K, eps, _dtype_code(X.dtype), _dtype_code(wt))
     return Y, mean, rstd
 
 
@@ -115,30 +128,21 @@ def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rs
     """(dX, dweight, dbias) from dY, the forward's X, mean and rstd (ss1_layernorm_backward). dweight and
     dbias have weight's dtype (X's without a weight). `need`: which of the three to compute (the
     others are None)."""
-    _tensor("X", X)
-    if X.dim() != 2 or X.shape[1] < 1:
-        raise ValueError("X must be [M, K] with K >= 1")
-    M, K = X.shape
-    _tensor("dY", dY, X.shape, X.dtype, X.device)
-    _tensor("mean", mean, (M,), torch.float32, X.device)
-    _tensor("rstd", rstd, (M,), torch.float32, X.device)
-    wt = _norm_weights(X, weight=weight)
-    on = _On(X.device, stream)
-    dX = torch.empty_like(X) if need[0] else None
-    dw = torch.empty(K, dtype=wt, device=X.device) if need[1] else None
-    db = torch.empty(K, dtype=wt, device=X.device) if need[2] else None
-    ws, size = None, 0
+    M, K = _norm_rows(X)
+    device = X.get_device()
+    _tensor("dY", dY, X.shape, X.dtype, device)
+    _tensor("mean", mean, X.shape[:1], torch.float32, device)
+    _tensor("rstd", rstd, X.shape[:1], torch.float32, device)
+    wt = _norm_weights(X, device, weight)
     L = lib()
-    if need[1] or need[2]:
-        n = ctypes.c_size_t()
-        _check(L.ss1_layernorm_backward_workspace(M, K, ctypes.byref(n)), "ss1_layernorm_backward_workspace")
-        size = n.value
-        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=X.device)
-    on.made(dX, dw, db, ws)
-    with on.guard:
-        _check(L.ss1_layernorm_backward(dY.data_ptr(), X.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight), _ptr(dX),
-                                        _ptr(dw), _ptr(db), M, K, _dtype_code(X.dtype), _dtype_code(wt), _ptr(ws), size,
-                                        on.handle), "ss1_layernorm_backward")
+    dX = torch.empty_like(X) if need[0] else None
+    dw = X.new_empty(K, dtype=wt) if need[1] else None
+    db = X.new_empty(K, dtype=wt) if need[2] else None
+    size = _norm_workspace(L, M, K) if need[1] or need[2] else 0
+    ws = X.new_empty(size, dtype=torch.uint8) if size else None
+    _call(device, stream, (dX, dw, db, ws), L.ss1_layernorm_backward, dY.data_ptr(), X.data_ptr(), mean.data_ptr(),
+          rstd.data_ptr(), _ptr(weight), _ptr(dX), _ptr(dw), _ptr(db), M, K, _dtype_code(X.dtype), _dtype_code(wt), _ptr(ws),
+          size)
     return dX, dw, db
 
 
@@ -164,11 +168,8 @@ class LayerNormFunction(torch.autograd.Function):
 
 # ---- low-rank adapters -----------------------------------------------------------------------
 
-class _Adapters(ctypes.Structure):
-    """ss1_adapters of include/ss1.h."""
-    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("index", ctypes.c_void_p),
-                ("plan", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("R", ctypes.c_int32),
-                ("count", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+#: ss1_adapters of include/ss1.h: A, B, scale, index, plan; K, N; R, count, dtype.
+_ADAPTERS = struct.Struct("@5P2q3i4x")
 
 
 class AdapterPlan:
@@ -178,51 +179,58 @@ class AdapterPlan:
         self.data, self.M, self.count = data, M, count
 
 
+@functools.lru_cache(maxsize=None)
+def _plan_bytes(L, M: int, count: int) -> int:
+    n = ctypes.c_size_t()
+    _check(L.ss1_adapter_plan_bytes(M, count, ctypes.byref(n)), "ss1_adapter_plan_bytes")
+    return n.value
+
+
 def adapter_plan(index: torch.Tensor, count: int, stream: Optional[torch.cuda.Stream] = None) -> AdapterPlan:
     """Plan of `index` (int32 [M]; outside [0, count): no adapter) for adapter_forward and adapter_backward."""
     _tensor("index", index, dtype=torch.int32)
     if index.dim() != 1:
         raise ValueError("index must be [M]")
-    M, n = index.shape[0], ctypes.c_size_t()
-    L = lib()
-    _check(L.ss1_adapter_plan_bytes(M, count, ctypes.byref(n)), "ss1_adapter_plan_bytes")
-    on = _On(index.device, stream)
-    data = torch.empty(n.value, dtype=torch.uint8, device=index.device)
-    on.made(data)
-    with on.guard:
-        _check(L.ss1_adapter_plan(index.data_ptr(), M, count, data.data_ptr(), n.value, on.handle), "ss1_adapter_plan")
+    M, L = index.shape[0], lib()
+    size = _plan_bytes(L, M, count)
+    data = index.new_empty(size, dtype=torch.uint8)
+    _call(index.get_device(), stream, (data,), L.ss1_adapter_plan, index.data_ptr(), M, count, data.data_ptr(), size)
     return AdapterPlan(data, M, count)
 
 
-def _adapters(X, A, B, index, scale, plan) -> _Adapters:
+@functools.lru_cache(maxsize=4096)
+def _adapter_workspace(L, M: int, K: int, N: int, R: int, n: int, dtype: int, backward: bool) -> int:
+    size = ctypes.c_size_t()
+    fwd, bwd = (None, ctypes.byref(size)) if backward else (ctypes.byref(size), None)
+    _check(L.ss1_adapter_workspace(M, K, N, R, n, dtype, fwd, bwd), "ss1_adapter_workspace")
+    return max(size.value, 1)
+
+
+def _adapters(X, A, B, index, scale, plan):
+    """(device, M, K, N, R, the packed ss1_adapters, dtype code, count) of checked arguments."""
     if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise ValueError("X must be [M, K], A [count, R, K] and B [count, N, R]")
     M, K = X.shape
     n, R, _ = A.shape
     N = B.shape[1]
+    device, t = X.get_device(), X.dtype
     _tensor("X", X)
-    _tensor("A", A, (n, R, K), X.dtype, X.device)
-    _tensor("B", B, (n, N, R), X.dtype, X.device)
+    _tensor("A", A, (n, R, K), t, device)
+    _tensor("B", B, (n, N, R), t, device)
     if not 1 <= R <= ADAPTER_MAX_RANK or not 1 <= n <= ADAPTER_MAX_COUNT:
         raise ValueError(f"ranks 1 .. {ADAPTER_MAX_RANK} and 1 .. {ADAPTER_MAX_COUNT} adapters, not {R} and {n}")
     if index is not None:
-        _tensor("index", index, (M,), torch.int32, X.device)
+        _tensor("index", index, (M,), torch.int32, device)
     elif n != 1:
         raise ValueError("several adapters need an index")
     if scale is not None:
-        _tensor("scale", scale, (n,), torch.float32, X.device)
-    if plan is not None:
-        if index is None or plan.M != M or plan.count != n or plan.data.device != X.device:
-            raise ValueError("the plan was made for another batch, count or device")
-    return _Adapters(A.data_ptr(), B.data_ptr(), _ptr(scale), _ptr(index), _ptr(plan.data) if plan is not None else None,
-                     K, N, R, n, _dtype_code(X.dtype))
-
-
-def _adapter_workspace(ad: _Adapters, M: int, backward: bool, device) -> torch.Tensor:
-    n = ctypes.c_size_t()
-    fwd, bwd = (None, ctypes.byref(n)) if backward else (ctypes.byref(n), None)
-    _check(lib().ss1_adapter_workspace(M, ad.K, ad.N, ad.R, ad.count, ad.dtype, fwd, bwd), "ss1_adapter_workspace")
-    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+        _tensor("scale", scale, (n,), torch.float32, device)
+    if plan is not None and (index is None or plan.M != M or plan.count != n or plan.data.get_device() != device):
+        raise ValueError("the plan was made for another batch, count or device")
+    code = int(_dtype_code(t))
+    packed = _ADAPTERS.pack(A.data_ptr(), B.data_ptr(), _ptr(scale) or 0, _ptr(index) or 0,
+                            plan.data.data_ptr() if plan is not None else 0, K, N, R, n, code)
+    return device, M, K, N, R, packed, code, n
 
 
 def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.Tensor, index: Optional[torch.Tensor] = None,
@@ -232,22 +240,20 @@ def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.
     projection's output Y [M, N], A [count, R, K], B [count, N, R], scale float32 [count]. index int32
     [M]; an entry outside [0, count) leaves its row as it is; None: every row uses the one adapter.
     `out` may be Y itself. keep: returns (out, H) with H = X A^T, float32 [M, R], for the backward pass."""
-    ad = _adapters(X, A, B, index, scale, plan)
-    M = X.shape[0]
-    _tensor("Y", Y, (M, ad.N), X.dtype, X.device)
-    on = _On(X.device, stream)
+    device, M, K, N, R, ad, code, n = _adapters(X, A, B, index, scale, plan)
+    _tensor("Y", Y, (M, N), X.dtype, device)
+    own = None
     if out is None:
-        out = torch.empty_like(Y)
-        on.made(out)
+        out = own = torch.empty_like(Y)
     else:
-        _tensor("out", out, Y.shape, Y.dtype, Y.device)
+        _tensor("out", out, Y.shape, Y.dtype, device)
         _apart(out, "out", X=X, A=A, B=B, Y=Y if out.data_ptr() != Y.data_ptr() else None)
-    H = torch.empty((M, ad.R), dtype=torch.float32, device=X.device) if keep else None
-    ws = _adapter_workspace(ad, M, False, X.device)
-    on.made(H, ws)
-    with on.guard:
-        _check(lib().ss1_adapter_forward(ctypes.byref(ad), X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
-                                         ws.data_ptr(), ws.numel(), on.handle), "ss1_adapter_forward")
+    H = X.new_empty((M, R), dtype=torch.float32) if keep else None
+    L = lib()
+    size = _adapter_workspace(L, M, K, N, R, n, code, False)
+    ws = X.new_empty(size, dtype=torch.uint8)
+    _call(device, stream, (own, H, ws), L.ss1_adapter_forward, ad, X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
+          ws.data_ptr(), size)
     return (out, H) if keep else out
 
 
@@ -258,25 +264,22 @@ def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torc
     """(dX, dA, dB) of adapter_forward for dY, the gradient of its output (ss1_adapter_backward). H is what
     the forward kept (needed for dB); `dX`, if given, is the projection's input gradient, which the
     result includes. `need`: which of the three to compute (the others are None)."""
-    ad = _adapters(X, A, B, index, scale, plan)
-    M = X.shape[0]
-    _tensor("dY", dY, (M, ad.N), X.dtype, X.device)
+    device, M, K, N, R, ad, code, n = _adapters(X, A, B, index, scale, plan)
+    _tensor("dY", dY, (M, N), X.dtype, device)
     if need[2]:
         if H is None:
             raise ValueError("dB needs H, which adapter_forward(keep=True) returns")
-        _tensor("H", H, (M, ad.R), torch.float32, X.device)
+        _tensor("H", H, (M, R), torch.float32, device)
     if dX is not None:
-        _tensor("dX", dX, X.shape, X.dtype, X.device)
-    on = _On(X.device, stream)
+        _tensor("dX", dX, X.shape, X.dtype, device)
     out = torch.empty_like(X) if need[0] else None
     dA = torch.empty_like(A) if need[1] else None
     dB = torch.empty_like(B) if need[2] else None
-    ws = _adapter_workspace(ad, M, True, X.device)
-    on.made(out, dA, dB, ws)
-    with on.guard:
-        _check(lib().ss1_adapter_backward(ctypes.byref(ad), dY.data_ptr(), X.data_ptr(), _ptr(H) if need[2] else None,
-                                          _ptr(dX) if need[0] else None, _ptr(out), _ptr(dA), _ptr(dB), M, ws.data_ptr(),
-                                          ws.numel(), on.handle), "ss1_adapter_backward")
+    L = lib()
+    size = _adapter_workspace(L, M, K, N, R, n, code, True)
+    ws = X.new_empty(size, dtype=torch.uint8)
+    _call(device, stream, (out, dA, dB, ws), L.ss1_adapter_backward, ad, dY.data_ptr(), X.data_ptr(),
+          H.data_ptr() if need[2] else None, _ptr(dX) if need[0] else None, _ptr(out), _ptr(dA), _ptr(dB), M, ws.data_ptr(), size)
     return out, dA, dB
 
 
@@ -330,13 +333,21 @@ def adamw_factors(step: int, lr: float = 1e-3, betas: Tuple[float, float] = (0.9
     return out
 
 
-def _same(name: str, ts: Sequence[torch.Tensor], like: Sequence[torch.Tensor], dtype, device):
-    if len(ts) != len(like):
-        raise ValueError(f"{name}: {len(ts)} tensors for {len(like)} parameters")
-    for t, p in zip(ts, like):
-        if t.numel() != p.numel() or t.device != device or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-            raise ValueError(f"{name} must be contiguous, on {device}, of its parameter's size" +
-                             (f" and {dtype}" if dtype is not None else ""))
+_POINTER, _NUMEL, _CONTIGUOUS, _DEVICE = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous,
+                                          torch.Tensor.get_device)
+_DTYPE = attrgetter("dtype")
+
+
+def _like(name: str, ts: Sequence[torch.Tensor], sizes: List[int], device: int, dtypes) -> List[int]:
+    """The tensors' addresses, after the checks."""
+    if list(map(_NUMEL, ts)) != sizes:
+        raise ValueError(f"{name}: one tensor for each parameter, of its size")
+    if set(map(_DEVICE, ts)) - {device} or not all(map(_CONTIGUOUS, ts)) or not set(map(_DTYPE, ts)) <= dtypes:
+        raise ValueError(f"{name} must be contiguous, on cuda:{device} and of " + " or ".join(map(str, dtypes)))
+    return list(map(_POINTER, ts))
+
+
+_WEIGHTS, _F32, _U8 = {torch.bfloat16, torch.float32}, {torch.float32}, {torch.uint8}
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor],
@@ -353,39 +364,37 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     n = len(params)
     if n == 0:
         return
-    device = params[0].device
-    if device.type != "cuda":
+    device = params[0].get_device()
+    if device < 0:
         raise ValueError("params must be CUDA tensors")
     bits = 32 if scales is None else 8
-    _same("params", params, params, None, device)
-    _same("grads", grads, params, None, device)
-    state = torch.float32 if bits == 32 else torch.uint8
-    _same("exp_avg", exp_avg, params, state, device)
-    _same("exp_avg_sq", exp_avg_sq, params, state, device)
+    sizes = list(map(_NUMEL, params))
     table = np.zeros(n, _ADAMW_TENSOR)
-    ptr = torch.Tensor.data_ptr
-    table["param"], table["grad"] = [ptr(t) for t in params], [ptr(t) for t in grads]
-    table["exp_avg"], table["exp_avg_sq"] = [ptr(t) for t in exp_avg], [ptr(t) for t in exp_avg_sq]
-    table["numel"] = [t.numel() for t in params]
-    table["param_dtype"], table["grad_dtype"] = [_dtype_code(t.dtype) for t in params], [_dtype_code(t.dtype) for t in grads]
+    table["param"] = _like("params", params, sizes, device, _WEIGHTS)
+    table["grad"] = _like("grads", grads, sizes, device, _WEIGHTS)
+    state = _F32 if bits == 32 else _U8
+    table["exp_avg"] = _like("exp_avg", exp_avg, sizes, device, state)
+    table["exp_avg_sq"] = _like("exp_avg_sq", exp_avg_sq, sizes, device, state)
+    table["numel"] = sizes
+    for field, ts in (("param_dtype", params), ("grad_dtype", grads)):
+        kinds = set(map(_DTYPE, ts))
+        table[field] = _dtype_code(kinds.pop()) if len(kinds) == 1 else [_dtype_code(t.dtype) for t in ts]
     if master is not None:
         if len(master) != n:
             raise ValueError(f"master: {len(master)} tensors for {n} parameters")
-        some = [i for i in range(n) if master[i] is not None]
-        _same("master", [master[i] for i in some], [params[i] for i in some], torch.float32, device)
-        table["master"] = [0 if t is None else ptr(t) for t in master]
+        some = [i for i, t in enumerate(master) if t is not None]
+        if len(some) == n:
+            table["master"] = _like("master", master, sizes, device, _F32)
+        elif some:
+            table["master"][some] = _like("master", [master[i] for i in some], [sizes[i] for i in some], device, _F32)
     if scales is not None:
-        for name, ts, field in (("scales[0]", scales[0], "avg_scale"), ("scales[1]", scales[1], "sq_scale")):
-            if len(ts) != n or any(s.numel() != -(-p.numel() // ADAMW_BLOCK) or s.dtype != torch.float32 or s.device != device
-                                   or not s.is_contiguous() for s, p in zip(ts, params)):
-                raise ValueError(f"{name} must be contiguous float32 [ceil(numel / {ADAMW_BLOCK})] a parameter, on {device}")
-            table[field] = [ptr(t) for t in ts]
+        blocks = [-(-size // ADAMW_BLOCK) for size in sizes]
+        table["avg_scale"] = _like("scales[0]", scales[0], blocks, device, _F32)
+        table["sq_scale"] = _like("scales[1]", scales[1], blocks, device, _F32)
     if factors is not None:
         _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
     hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
-    on = _On(device, stream)
-    with on.guard:
-        _check(lib().ss1_adamw_step(table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), on.handle), "ss1_adamw_step")
+    _call(device, stream, (), lib().ss1_adamw_step, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors))
 
 
 class AdamW:
@@ -400,7 +409,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         for i, p in enumerate(self.params):
-            _tensor(f"params[{i}]", p, device=self.params[0].device)
+            _tensor(f"params[{i}]", p, device=self.params[0].get_device())
             _dtype_code(p.dtype)
             if any(q is p for q in self.params[:i]):
                 raise ValueError(f"params[{i}] is in the list twice")

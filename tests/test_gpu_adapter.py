@@ -186,7 +186,7 @@ def test_plan_lists_the_rows(ops, M, n):
     plan = ops.adapter_plan(index, n)
     torch.cuda.synchronize()
     data = plan.data.cpu().view(torch.int32)
-    head, tiles = (n + 2 + 3) // 4 * 4, M // 128 + n + 1
+    head, tiles = 2 * ((n + 2 + 3) // 4 * 4), M // 128 + n + 1
     first, rows = data[:n + 2], data[head + 4 * tiles:head + 4 * tiles + M]
     idx = index.cpu()
     group = torch.where((idx >= 0) & (idx < n), idx, n)
@@ -194,6 +194,8 @@ def test_plan_lists_the_rows(ops, M, n):
     assert torch.equal(rows.long(), order)
     counts = torch.bincount(group.long(), minlength=n + 1)
     assert torch.equal(first[1:].long(), counts.cumsum(0)) and first[0] == 0
+    per = [0] + [-(-int(c) // 128) for c in counts]
+    assert torch.equal(data[head // 2:head // 2 + n + 2].long(), torch.tensor(per).cumsum(0))
     got = data[head:head + 4 * tiles].reshape(-1, 4)
     want = [(a if a < n else -1, int(first[a]) + i, min(128, int(counts[a]) - i)) for a in range(n + 1) for i in range(0, int(counts[a]), 128)]
     assert [tuple(r[:3].tolist()) for r in got[:len(want)]] == want and not got[len(want):, 2].any()

@@ -59,10 +59,8 @@ def test_layernorm_backward(lib):
 
 def _adapters(**change):
     from structured_compressed_linear_b200 import ops
-    a = ops._Adapters(P, P, P, P, None, 64, 32, 8, 3, 0)
-    for k, v in change.items():
-        setattr(a, k, v)
-    return a
+    fields = dict(A=P, B=P, scale=P, index=P, plan=None, K=64, N=32, R=8, count=3, dtype=0)
+    return ops._ADAPTERS.pack(*(v or 0 for v in dict(fields, **change).values()))
 
 
 BAD_ADAPTERS = [dict(R=0), dict(R=129), dict(count=0), dict(count=1025), dict(K=0), dict(N=0), dict(K=(1 << 24) + 1), dict(dtype=2),
@@ -92,7 +90,7 @@ def test_adapter_forward(lib):
 
     def call(ad=None, **change):
         ad = _adapters(**(ad or {}))
-        return lib.ss1_adapter_forward(ctypes.byref(ad), *dict(ok, **change).values())
+        return lib.ss1_adapter_forward(ad, *dict(ok, **change).values())
     assert call(M=0) == 0
     assert lib.ss1_adapter_forward(None, *ok.values()) == -1
     for bad in BAD_ADAPTERS:
@@ -112,7 +110,7 @@ def test_adapter_backward(lib):
 
     def call(ad=None, **change):
         ad = _adapters(**(ad or {}))
-        return lib.ss1_adapter_backward(ctypes.byref(ad), *dict(ok, **change).values())
+        return lib.ss1_adapter_backward(ad, *dict(ok, **change).values())
     assert call(dX_in=None, dX=None, dA=None, dB=None) == 0
     for bad in BAD_ADAPTERS:
         assert call(ad=bad) == -1, bad
@@ -196,7 +194,7 @@ def test_structs_match_header(tmp_path):
     subprocess.run([gcc, "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     f = ops._ADAMW_TENSOR.fields
-    assert got == [ctypes.sizeof(ops._Adapters), ops._Adapters.K.offset, ops._Adapters.dtype.offset, ops._ADAMW_TENSOR.itemsize,
+    assert got == [ops._ADAPTERS.size, 40, 64, ops._ADAMW_TENSOR.itemsize,
                    f["numel"][1], f["grad_dtype"][1], ctypes.sizeof(ops._AdamWHyper)]
 
 
