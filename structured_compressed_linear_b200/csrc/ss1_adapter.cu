@@ -380,8 +380,12 @@ cudaError_t plan_of(const ss1_adapters& ad, int64_t M, void* ws, Call& c, cudaSt
     return ad.plan ? cudaSuccess : launch_plan(ad.index, M, ad.count, c.plan, st);
 }
 
-// Rows up to which the general kernels serve bf16 calls too.
-constexpr int64_t kGeneralRows = 32;
+// Rows up to which a forward runs a row a cluster.
+constexpr int64_t kFewRows = 64;
+
+bool rows_shape(const ss1_adapters& ad, int64_t M) {
+    return M <= kFewRows && ad.K % 8 == 0 && ad.N % 8 == 0 && ad.R % 8 == 0 && aligned(ad.A, 16) && aligned(ad.B, 16);
+}
 
 }  // namespace
 
@@ -453,7 +457,12 @@ extern "C" SS1_API int ss1_adapter_forward(const ss1_adapters* ad, const void* X
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     Call c = call_of(*ad, M);
     cudaError_t err = cudaSuccess;
-    if (M > kGeneralRows && mma_shape(*ad, M) && aligned(X, 16) && aligned(Y, 16) && aligned(out, 16)) {
+    const bool vec = aligned(X, 16) && aligned(Y, 16) && aligned(out, 16);
+    if (vec && rows_shape(*ad, M)) {
+        if (rows_forward(c, X, Y, out, H, ad->dtype, st) != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
+        return SS1_OK;
+    }
+    if (vec && mma_shape(*ad, M)) {
         err = plan_of(*ad, M, ws, c, st);
         const MmaSpace w{ws + s.plan, nullptr, ws + s.plan + s.packed, nullptr, nullptr, nullptr};
         if (err == cudaSuccess) err = mma_forward(c, X, Y, out, H, w, st);
@@ -491,7 +500,7 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     Call c = call_of(*ad, M);
     err = plan_of(*ad, M, ws, c, st);
-    if (err == cudaSuccess && M > kGeneralRows && mma_shape(*ad, M) && aligned(dY, 16) && aligned(X, 16) && aligned(dX_in, 16) &&
+    if (err == cudaSuccess && mma_shape(*ad, M) && aligned(dY, 16) && aligned(X, 16) && aligned(dX_in, 16) &&
         aligned(dX, 16)) {
         uint8_t* at = ws + s.plan;
         MmaSpace w;

@@ -39,6 +39,9 @@ struct Call {
 // Shares of an adapter's rows in the sums of dA and dB (general path).
 int general_shares(int64_t M, int64_t C, int R, int n);
 
+// Forward for a few rows (ss1_adapter_rows.cu): K, N and R multiples of 8, 16-byte aligned rows, either type.
+cudaError_t rows_forward(const Call& c, const void* X, const void* Y, void* out, float* H, int dtype, cudaStream_t st);
+
 // Tensor-core path (ss1_adapter_mma.cu): bf16, K and N multiples of 8, 16-byte aligned rows.
 struct MmaSpace {
     void *packed_g, *packed_h;   // [M][2][mma_rank(R)] bf16 in plan order, two parts each: s H (forward) or G; s H beside it

@@ -160,16 +160,23 @@ struct ProductsShape {
 template <int RT, bool TRANS>
 __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restrict__ U, const bf16* __restrict__ table, int ld,
                                                             const float* __restrict__ scale, PlanView plan, float* __restrict__ H,
-                                                            bf16* __restrict__ packed, int M, int C, int R, int n) {
+                                                            bf16* __restrict__ packed, int M, int C, int R, int n,
+                                                            bool table_is_new) {
     using S = ProductsShape<RT, TRANS>;
     extern __shared__ uint8_t raw[];
     let_next_start();
-    wait_for_previous();   // the prepared B; all of this grid waits, so that the next one need not look further back
+    // the widened B is the previous kernel's. Otherwise only the outputs' memory is shared with what ran before, and
+    // every CTA still waits before it ends, so that the next kernel need not look further back than this one.
+    if (table_is_new) wait_for_previous();
     const Tile tile = tile_of(plan, blockIdx.y, M);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int splits = gridDim.x, split = blockIdx.x;
-    if (tile.rows <= 0 || tile.adapter >= n) return;           // the whole cluster
+    if (tile.rows <= 0 || tile.adapter >= n) {                 // the whole cluster
+        wait_for_previous();
+        return;
+    }
     if (tile.adapter < 0) {                                    // no adapter: H is 0, nobody reads the packed rows
+        wait_for_previous();
         if (H)
             for (int i = split * kThreads + tid; i < tile.rows * R; i += splits * kThreads) {
                 const int m = row_at(plan, tile.first + i / R, M);
@@ -279,6 +286,7 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
                 for (int i = 0; i < 4; ++i) sum[j][i] += acc[j][i];
         }
     ptx::cp_async_wait<0>();
+    wait_for_previous();
     __syncthreads();
     // the partial products over the ring's memory
     float* part = reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw)));
@@ -759,7 +767,7 @@ int stage_splits(int64_t C, int tiles, int ctas) {
 // the kernels read it.
 template <int RT>
 cudaError_t prepare(const Call& c, const MmaSpace& w, const float* H, bool turn_a, bool with_b, const void** B, int* ld,
-                    cudaStream_t st) {
+                    bool* launched, cudaStream_t st) {
     Prepare d = {};
     d.ld = (c.R + 7) / 8 * 8;
     *ld = d.ld;
@@ -778,13 +786,15 @@ cudaError_t prepare(const Call& c, const MmaSpace& w, const float* H, bool turn_
         d.A = (const bf16*)c.A; d.turned_a = (bf16*)w.turned_a; d.K = (int)c.K;
         d.na = ctas((c.K + 31) / 32 * ((d.ld + 31) / 32) * c.n);
     }
-    if (d.nh + d.nb + d.na == 0) return cudaSuccess;
+    *launched = d.nh + d.nb + d.na > 0;
+    if (!*launched) return cudaSuccess;
     prepare_kernel<RT><<<(unsigned)(d.nh + d.nb + d.na), kThreads, 0, st>>>(d, c.plan, (int)c.M, c.R, c.n);
     return cudaGetLastError();
 }
 
 template <int RT, bool TRANS>
-cudaError_t products(const Call& c, const void* U, const void* table, int ld, int64_t C, float* H, void* packed, cudaStream_t st) {
+cudaError_t products(const Call& c, const void* U, const void* table, int ld, int64_t C, float* H, void* packed, bool after_prepare, bool table_is_new,
+                     cudaStream_t st) {
     using S = ProductsShape<RT, TRANS>;
     auto* fn = &products_kernel<RT, TRANS>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
@@ -805,17 +815,19 @@ cudaError_t products(const Call& c, const void* U, const void* table, int ld, in
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = TRANS ? 2 : 1;                     // backward: after prepare_kernel
+    cfg.numAttrs = after_prepare ? 2 : 1;             // only prepare_kernel may still be running
     return cudaLaunchKernelEx(&cfg, fn, (const bf16*)U, (const bf16*)table, ld, c.scale, c.plan, H, (bf16*)packed, (int)c.M, (int)C, c.R,
-                              c.n);
+                              c.n, table_is_new);
 }
 
 template <int RT>
 cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st) {
     int ld;
     const void* B;
-    cudaError_t e = prepare<RT>(c, w, nullptr, false, true, &B, &ld, st);
-    if (e == cudaSuccess) e = products<RT, false>(c, X, c.A, c.R, c.K, H, w.packed_g, st);
+    bool launched;
+    cudaError_t e = prepare<RT>(c, w, nullptr, false, true, &B, &ld, &launched, st);
+    // update_kernel reads B before it waits: what widened it has to be over when the products start
+    if (e == cudaSuccess) e = products<RT, false>(c, X, c.A, c.R, c.K, H, w.packed_g, false, false, st);
     using S = UpdateShape<RT>;
     auto* fn = &update_kernel<RT>;
     if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
@@ -830,8 +842,9 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
                         const MmaSpace& w, cudaStream_t st) {
     int ld;
     const void* B;
-    cudaError_t e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, st);
-    if (e == cudaSuccess && (dX || dA)) e = products<RT, true>(c, dY, B, ld, c.N, nullptr, w.packed_g, st);
+    bool launched;
+    cudaError_t e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, &launched, st);
+    if (e == cudaSuccess && (dX || dA)) e = products<RT, true>(c, dY, B, ld, c.N, nullptr, w.packed_g, launched, B != c.B, st);
     auto* fn = &gradients_kernel<RT>;
     if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), gradients_smem<RT>());
     if (e != cudaSuccess) return e;
