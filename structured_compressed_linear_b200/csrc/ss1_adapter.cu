@@ -347,10 +347,10 @@ Sizes workspace_of(int64_t M, int64_t K, int64_t N, int R, int n) {
 }
 
 // The tensor-core path takes bf16 rows on 16-byte boundaries (and B's rows too, where R allows it), and as
-// many tiles as a grid's second dimension.
+// many tiles and column ranges as a grid's second dimension.
 bool mma_shape(const ss1_adapters& ad, int64_t M) {
     return ad.dtype == SS1_DTYPE_BF16 && ad.K % 8 == 0 && ad.N % 8 == 0 && aligned(ad.A, 16) && (ad.R % 8 || aligned(ad.B, 16)) &&
-           max_tiles(M, ad.count) <= 65535;
+           max_tiles(M, ad.count) <= 32768 && ad.K <= 1 << 22 && ad.N <= 1 << 22;
 }
 
 // What the calls have in common; `status` other than SS1_OK refuses.
@@ -380,11 +380,15 @@ cudaError_t plan_of(const ss1_adapters& ad, int64_t M, void* ws, Call& c, cudaSt
     return ad.plan ? cudaSuccess : launch_plan(ad.index, M, ad.count, c.plan, st);
 }
 
-// Rows up to which a forward runs a row a cluster.
-constexpr int64_t kFewRows = 64;
+// A forward runs a row a cluster up to kFewRows rows, while these read no more than kFewWork elements of A and B
+// (each row reads its own). Measured as graph replays, that and the tensor-core kernels (with their
+// plan), us: K = N = 4096, R = 16, 24 adapters: 5.3 / 13.9 at 48 rows, 6.4 / 14.2 at 64, 15.8 / 14.8 at 192;
+// K = 4096, N = 14336, R = 16: 8.6 / 13.9 at 48 rows, 16.7 / 14.7 at 96; R = 64, N = 4096: 9.2 / 14.3 at 16 rows,
+// 15.0 / 14.4 at 48. One adapter of rank 8 on 768 x 2304 (no plan): 4.6 / 6.5 at 64 rows, 7.5 / 7.2 at 96.
+constexpr int64_t kFewRows = 64, kFewWork = 1 << 24;
 
 bool rows_shape(const ss1_adapters& ad, int64_t M) {
-    return M <= kFewRows && ad.K % 8 == 0 && ad.N % 8 == 0 && ad.R % 8 == 0 && aligned(ad.A, 16) && aligned(ad.B, 16);
+    return M <= kFewRows && M * ad.R * (ad.K + ad.N) <= kFewWork && ad.K % 8 == 0 && ad.N % 8 == 0 && ad.R % 8 == 0 && aligned(ad.A, 16) && aligned(ad.B, 16);
 }
 
 }  // namespace

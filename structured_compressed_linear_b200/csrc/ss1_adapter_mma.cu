@@ -157,18 +157,29 @@ struct ProductsShape {
     static constexpr int smem = (ring > sums ? ring : sums) + 128;
 };
 
+struct Products {
+    const bf16* U;
+    const bf16* table;
+    const float* scale;      // of `packed`
+    float* H;                // unscaled, by batch row; or null
+    bf16* packed;
+    int C, ld;
+    bool table_is_new;
+};
+
 template <int RT, bool TRANS>
-__global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restrict__ U, const bf16* __restrict__ table, int ld,
-                                                            const float* __restrict__ scale, PlanView plan, float* __restrict__ H,
-                                                            bf16* __restrict__ packed, int M, int C, int R, int n,
-                                                            bool table_is_new) {
+__device__ __forceinline__ void products_role(const Products& d, const PlanView& plan, int tile_index, uint8_t* raw, int M, int R,
+                                              int n) {
     using S = ProductsShape<RT, TRANS>;
-    extern __shared__ uint8_t raw[];
-    let_next_start();
+    const bf16 *U = d.U, *table = d.table;
+    const float* scale = d.scale;
+    float* H = d.H;
+    bf16* packed = d.packed;
+    const int C = d.C, ld = d.ld;
     // the widened B is the previous kernel's. Otherwise only the outputs' memory is shared with what ran before, and
     // every CTA still waits before it ends, so that the next kernel need not look further back than this one.
-    if (table_is_new) wait_for_previous();
-    const Tile tile = tile_of(plan, blockIdx.y, M);
+    if (d.table_is_new) wait_for_previous();
+    const Tile tile = tile_of(plan, tile_index, M);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int splits = gridDim.x, split = blockIdx.x;
     if (tile.rows <= 0 || tile.adapter >= n) {                 // the whole cluster
@@ -328,6 +339,13 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const bf16* __restri
         }
     }
     if (splits > 1) ptx::cluster_sync();   // nobody leaves while its sums are being read
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads) products_kernel(const Products d, PlanView plan, int M, int R, int n) {
+    extern __shared__ uint8_t raw[];
+    let_next_start();
+    products_role<RT, false>(d, plan, blockIdx.y, raw, M, R, n);
 }
 
 // ---- update ----------------------------------------------------------------------------------
@@ -700,28 +718,45 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
     ptx::cp_async_wait<0>();
 }
 
-// dB, dA and dX in one launch: each needs only G and what prepare_kernel wrote, and their streams overlap.
-// CTAs 0 .. nb - 1 take dB (dY, just read for G, is partly still in L2), then na take dA, the rest dX.
+// G and dB in one launch: both read dY (from HBM once: the other reader finds it in L2). The first `tiles` rows of
+// the grid are G's clusters; the CTAs behind them, as many as dB has, take its columns and runs.
 template <int RT>
-constexpr int gradients_smem() {
+constexpr int first_smem() {
+    return ColumnsShape<RT>::smem > ProductsShape<RT, true>::smem ? ColumnsShape<RT>::smem : ProductsShape<RT, true>::smem;
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) first_gradients_kernel(const Products g, int tiles, const Columns db, int nb,
+                                                                                     PlanView plan, int M, int R, int n) {
+    extern __shared__ uint8_t raw[];
+    let_next_start();
+    if ((int)blockIdx.y < tiles) {
+        products_role<RT, true>(g, plan, blockIdx.y, raw, M, R, n);
+    } else {
+        wait_for_previous();      // the packed H
+        const int k = ((int)blockIdx.y - tiles) * gridDim.x + blockIdx.x, ranges = (db.C + kColCols - 1) / kColCols;
+        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, M, R, n);
+    }
+}
+
+// dA and dX in one launch: both need G. CTAs 0 .. na - 1 take dA, the rest dX.
+template <int RT>
+constexpr int second_smem() {
     return ColumnsShape<RT>::smem > UpdateShape<RT>::smem ? ColumnsShape<RT>::smem : UpdateShape<RT>::smem;
 }
 
 template <int RT>
-__global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) gradients_kernel(const Columns db, int nb, const Columns da, int na,
-                                                                               const Update dx, PlanView plan, int M, int R, int n) {
+__global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_kernel(const Columns da, int na, const Update dx,
+                                                                                      PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
     let_next_start();
     wait_for_previous();
     const int i = blockIdx.x;
-    if (i < nb + na) {
-        const bool b = i < nb;
-        const Columns& d = b ? db : da;
-        const int ranges = (d.C + kColCols - 1) / kColCols, k = b ? i : i - nb;
-        columns_role<RT>(d, plan, k % ranges, k / ranges, raw, M, R, n);
+    if (i < na) {
+        const int ranges = (da.C + kColCols - 1) / kColCols;
+        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, M, R, n);
     } else {
-        const int k = i - nb - na;
-        update_role<RT>(dx, plan, tile_of(plan, k / dx.splits, M), k % dx.splits, raw, M, R, n, true);
+        update_role<RT>(dx, plan, tile_of(plan, (i - na) / dx.splits, M), (i - na) % dx.splits, raw, M, R, n, true);
     }
 }
 
@@ -756,12 +791,16 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const Sums s, PlanView pl
 int tiles_at_most(const Call& c) { return c.plan.rows ? c.plan.max_tiles : (int)((c.M + kTile - 1) / kTile); }
 
 // Shares of the columns for `tiles` row tiles: about `ctas` CTAs in all, at least four 64-column stages each.
-int stage_splits(int64_t C, int tiles, int ctas) {
-    const int most = (int)((C + 255) / 256);
+int stage_splits(int64_t C, int tiles, int ctas, int most) {
+    const int stages = (int)((C + 255) / 256);
     int s = ctas / tiles;
+    s = s > stages ? stages : s;
     s = s > most ? most : s;
     return s < 1 ? 1 : s;
 }
+
+// CTAs of each part of the backward's two launches
+constexpr int kFirstCtas = 148, kColumnsCtas = 148, kUpdateCtas = 296;
 
 // H packed and A transposed where the pointers are given, B widened where R is no multiple of 8; *B and *ld: B as
 // the kernels read it.
@@ -792,73 +831,82 @@ cudaError_t prepare(const Call& c, const MmaSpace& w, const float* H, bool turn_
     return cudaGetLastError();
 }
 
-template <int RT, bool TRANS>
-cudaError_t products(const Call& c, const void* U, const void* table, int ld, int64_t C, float* H, void* packed, bool after_prepare, bool table_is_new,
-                     cudaStream_t st) {
-    using S = ProductsShape<RT, TRANS>;
-    auto* fn = &products_kernel<RT, TRANS>;
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
-    if (e != cudaSuccess) return e;
-    const int tiles = tiles_at_most(c);
-    int splits = stage_splits(C, tiles, 296);
-    splits = splits > 8 ? 8 : splits;                 // clusters of a portable size
+// A launch of clusters of (x, 1, 1) CTAs; `dependent`: it may start while the previous kernel drains.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*fn)(P...), dim3 grid, int x, size_t smem, bool dependent, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)splits, (unsigned)tiles);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::smem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)splits;
+    at[0].val.clusterDim.x = (unsigned)x;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = after_prepare ? 2 : 1;             // only prepare_kernel may still be running
-    return cudaLaunchKernelEx(&cfg, fn, (const bf16*)U, (const bf16*)table, ld, c.scale, c.plan, H, (bf16*)packed, (int)c.M, (int)C, c.R,
-                              c.n, table_is_new);
+    cfg.numAttrs = dependent ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
+
+constexpr int kPortableCluster = 8;
 
 template <int RT>
 cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st) {
+    using SP = ProductsShape<RT, false>;
+    using SU = UpdateShape<RT>;
+    auto* pfn = &products_kernel<RT>;
+    auto* ufn = &update_kernel<RT>;
     int ld;
     const void* B;
     bool launched;
-    cudaError_t e = prepare<RT>(c, w, nullptr, false, true, &B, &ld, &launched, st);
-    // update_kernel reads B before it waits: what widened it has to be over when the products start
-    if (e == cudaSuccess) e = products<RT, false>(c, X, c.A, c.R, c.K, H, w.packed_g, false, false, st);
-    using S = UpdateShape<RT>;
-    auto* fn = &update_kernel<RT>;
-    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), S::smem);
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(pfn), SP::smem);
+    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(ufn), SU::smem);
+    if (e == cudaSuccess) e = prepare<RT>(c, w, nullptr, false, true, &B, &ld, &launched, st);
     if (e != cudaSuccess) return e;
-    const int tiles = tiles_at_most(c), splits = stage_splits(c.N, tiles, 296);
-    const Update d{(const bf16*)w.packed_g, (const bf16*)B, (const bf16*)Y, (bf16*)out, (int)c.N, ld, splits};
-    return launch_dependent(fn, dim3((unsigned)splits, (unsigned)tiles), dim3(kThreads), S::smem, st, d, c.plan, (int)c.M, c.R, c.n);
+    const int tiles = tiles_at_most(c);
+    const int psplits = stage_splits(c.K, tiles, 296, kPortableCluster), usplits = stage_splits(c.N, tiles, 296, 1 << 20);
+    const Products p{(const bf16*)X, (const bf16*)c.A, c.scale, H, (bf16*)w.packed_g, (int)c.K, c.R, false};
+    // update_kernel reads B before it waits: what widened it has to be over when the products start
+    e = launch_clusters(pfn, dim3((unsigned)psplits, (unsigned)tiles), psplits, SP::smem, false, st, p, c.plan, (int)c.M, c.R, c.n);
+    if (e != cudaSuccess) return e;
+    const Update d{(const bf16*)w.packed_g, (const bf16*)B, (const bf16*)Y, (bf16*)out, (int)c.N, ld, usplits};
+    return launch_dependent(ufn, dim3((unsigned)usplits, (unsigned)tiles), dim3(kThreads), SU::smem, st, d, c.plan, (int)c.M, c.R, c.n);
 }
 
 template <int RT>
 cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
                         const MmaSpace& w, cudaStream_t st) {
+    auto* fn1 = &first_gradients_kernel<RT>;
+    auto* fn2 = &second_gradients_kernel<RT>;
     int ld;
     const void* B;
-    bool launched;
-    cudaError_t e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, &launched, st);
-    if (e == cudaSuccess && (dX || dA)) e = products<RT, true>(c, dY, B, ld, c.N, nullptr, w.packed_g, launched, B != c.B, st);
-    auto* fn = &gradients_kernel<RT>;
-    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn), gradients_smem<RT>());
+    bool prepared;
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn1), first_smem<RT>());
+    if (e == cudaSuccess) e = smem_attr_once(reinterpret_cast<const void*>(fn2), second_smem<RT>());
+    if (e == cudaSuccess) e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, &prepared, st);
     if (e != cudaSuccess) return e;
     const int rb = mma_runs(c.M, c.N, c.n), ra = mma_runs(c.M, c.K, c.n);
     const Columns db{(const bf16*)dY, (const bf16*)w.packed_h, (bf16*)dB, w.part_b, (int)c.N, c.R, 1, rb};
     const Columns da{(const bf16*)X, (const bf16*)w.packed_g, (bf16*)dA, w.part_a, (int)c.K, 1, (int)c.K, ra};
     const int nb = dB ? (db.C + kColCols - 1) / kColCols * rb : 0;
     const int na = dA ? (da.C + kColCols - 1) / kColCols * ra : 0;
-    const int tiles = tiles_at_most(c);
-    const Update dx{(const bf16*)w.packed_g, (const bf16*)w.turned_a, (const bf16*)dX_in, (bf16*)dX, (int)c.K, ld, stage_splits(c.K, tiles, 148)};
-    const int64_t ctas = (int64_t)nb + na + (dX ? (int64_t)tiles * dx.splits : 0);
-    e = launch_dependent(fn, dim3((unsigned)ctas), dim3(kThreads), gradients_smem<RT>(), st, db, nb, da, na, dx, c.plan, (int)c.M, c.R,
-                         c.n);
-    if (e != cudaSuccess || (!dA && !dB)) return e;
+    const int tiles = tiles_at_most(c), gtiles = dX || dA ? tiles : 0;
+    const int splits = stage_splits(c.N, tiles, kFirstCtas, kPortableCluster);
+    const Products g{(const bf16*)dY, (const bf16*)B, c.scale, nullptr, (bf16*)w.packed_g, (int)c.N, ld, B != c.B};
+    e = launch_clusters(fn1, dim3((unsigned)splits, (unsigned)(gtiles + (nb + splits - 1) / splits)), splits, first_smem<RT>(), prepared, st,
+                        g, gtiles, db, nb, c.plan, (int)c.M, c.R, c.n);
+    if (e != cudaSuccess) return e;
+    if (dX || dA) {
+        const Update dx{(const bf16*)w.packed_g, (const bf16*)w.turned_a, (const bf16*)dX_in, (bf16*)dX, (int)c.K, ld,
+                        stage_splits(c.K, tiles, kUpdateCtas, 1 << 20)};
+        const int64_t ctas = (int64_t)na + (dX ? (int64_t)tiles * dx.splits : 0);
+        e = launch_dependent(fn2, dim3((unsigned)ctas), dim3(kThreads), second_smem<RT>(), st, da, na, dx, c.plan, (int)c.M, c.R, c.n);
+        if (e != cudaSuccess) return e;
+    }
+    if (!dA && !dB) return cudaSuccess;
     Sums s = {};
     if (dA) { s.part[0] = da.part; s.out[0] = da.out; s.size[0] = (int64_t)c.K * c.R; s.runs[0] = ra; }
     if (dB) { s.part[1] = db.part; s.out[1] = db.out; s.size[1] = (int64_t)c.N * c.R; s.runs[1] = rb; }
@@ -872,9 +920,8 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
 int mma_rank(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
 
 int mma_runs(int64_t M, int64_t C, int n) {
-    // a quarter of two CTAs for each of 148 SMs (dB and dA each move half of dX's bytes), at least two
-    // tiles a run
-    int64_t s = 74 / ((C + kColCols - 1) / kColCols);
+    // at least two tiles a run
+    int64_t s = kColumnsCtas / ((C + kColCols - 1) / kColCols);
     const int64_t most = (M / kTile + 1) / 2;
     s = s > most ? most : s;
     return (int)(s < 1 ? 1 : s);
