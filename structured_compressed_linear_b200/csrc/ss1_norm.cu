@@ -11,6 +11,7 @@
 // registers, not over memory), never from sum x^2 - mean^2, which loses all digits where |mean|
 // is large. All sums are float32.
 #include "ss1_ops.cuh"
+#include "ptx_sm100.cuh"
 
 namespace ss1 {
 namespace {
@@ -21,107 +22,213 @@ constexpr int kUnit = 8;   // elements a thread takes at a time: 16 bytes of bf1
 
 // Eight elements of a row. Vector form: consecutive, from 8 * (unit * width + t); scalar form (rows
 // that do not start on 16-byte boundaries): strided by the width, so that a warp's loads stay
-// together. `n` is what is left of the row from the unit's first element.
+// together. They are worked on as four pairs.
 template <bool VEC>
 __device__ __forceinline__ int unit_first(int unit, int width, int t) {
     return VEC ? (unit * width + t) * kUnit : unit * width * kUnit + t;
 }
 
+// `p` is the row (or the weights), `left` what `total` leaves behind it; elements past K are `other`.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_unit(const T* __restrict__ p, int64_t base, int64_t total, int first, int width,
-                                          int K, float (&f)[kUnit], int site) {
+__device__ __forceinline__ void load_unit(const T* __restrict__ p, [[maybe_unused]] int64_t left, int first, int width, int K, F2 (&f)[4],
+                                          float other, int site) {
     if (VEC) {
-        Raw8<T> r;
-        if (first < K && SS1_SPAN_IN(base + first, kUnit, total, site)) r.load(p + base + first);
-        else r.zero();
-        r.get(f);
+        if (first < K && SS1_SPAN_IN(first, kUnit, left, site)) {
+            Raw8<T> r;
+            r.load(p + first);
+            r.get(f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = F2::both(other);
+        }
     } else {
+        float v[kUnit];
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
             const int k = first + i * width;
-            f[i] = k < K && SS1_IN(base + k, total, site) ? to_f(p[base + k]) : 0.0f;
+            v[i] = k < K && SS1_IN(k, left, site) ? to_f(p[k]) : other;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = F2::of(v[2 * i], v[2 * i + 1]);
     }
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_unit(T* __restrict__ p, int64_t base, int64_t total, int first, int width, int K,
-                                           const float (&f)[kUnit], int site) {
+__device__ __forceinline__ void store_unit(T* __restrict__ p, [[maybe_unused]] int64_t left, int first, int width, int K,
+                                           const F2 (&f)[4], int site) {
     if (VEC) {
         Raw8<T> r;
         r.set(f);
-        if (first < K && SS1_SPAN_IN(base + first, kUnit, total, site)) r.store(p + base + first);
+        if (first < K && SS1_SPAN_IN(first, kUnit, left, site)) r.store(p + first);
     } else {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
             const int k = first + i * width;
-            if (k < K && SS1_IN(base + k, total, site)) p[base + k] = from_f<T>(f[i]);
+            if (k < K && SS1_IN(k, left, site)) p[k] = from_f<T>(i % 2 ? f[i / 2].hi() : f[i / 2].lo());
         }
     }
 }
 
+// Rows on their way (vector form): every thread copies the units that it will work on into places of its own
+// in shared memory, some rows ahead, and reads them back itself. So the bytes in flight cost no
+// registers, and a thread waits for its own copies only, without a barrier. A piece is 16 bytes a
+// thread, threads side by side.
+template <typename T>
+constexpr int pieces() { return kUnit * (int)sizeof(T) / 16; }   // 16-byte pieces of a unit
+
+template <typename T>
+__device__ __forceinline__ void unit_ahead(uint32_t place, int threads, const T* p, bool ok) {
+#pragma unroll
+    for (int i = 0; i < pieces<T>(); ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place + i * threads * 16), "l"(p + i * (16 / sizeof(T))),
+                     "r"(ok ? 16 : 0)
+                     : "memory");
+}
+__device__ __forceinline__ void unit_back(const uint8_t* place, int, Raw8<__nv_bfloat16>& r) { r.a = *reinterpret_cast<const uint4*>(place); }
+__device__ __forceinline__ void unit_back(const uint8_t* place, int threads, Raw8<float>& r) {
+    r.a = *reinterpret_cast<const float4*>(place);
+    r.b = *reinterpret_cast<const float4*>(place + threads * 16);
+}
+
 // Sum over the `width` threads of a row (one warp, or all warps of the CTA), the same in every
-// thread. `buf` holds one float per warp.
+// thread. `buf` holds one float per warp, zeros behind the last; uses of one buffer lie a barrier apart.
 __device__ __forceinline__ float row_sum(float v, int width, float* buf) {
     v = warp_sum(v);
     if (width == 32) return v;
-    const int warps = width / 32;
-    __syncthreads();   // the buffer's last use is over
     if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
     __syncthreads();
-    return warp_sum(threadIdx.x % 32 < warps ? buf[threadIdx.x % 32] : 0.0f);
+    if (width > 256) return warp_sum(buf[threadIdx.x % 32]);
+    const float4 a = *reinterpret_cast<const float4*>(buf);
+    v = (a.x + a.y) + (a.z + a.w);
+    if (width > 128) {
+        const float4 b = *reinterpret_cast<const float4*>(buf + 4);
+        v += (b.x + b.y) + (b.z + b.w);
+    }
+    return v;
 }
 
 // ---- forward ---------------------------------------------------------------------------------
 
-// One row per warp (`width` 32, several rows a CTA) or per CTA (`width` = blockDim.x), held in NU
-// units a thread.
-template <typename T, typename W, bool VEC, int NU>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* __restrict__ X, const W* __restrict__ w,
-                                                        const W* __restrict__ b, T* __restrict__ Y,
-                                                        float* __restrict__ mean_out, float* __restrict__ rstd_out,
-                                                        int64_t M, int K, float eps, int width) {
-    __shared__ float buf[32];
-    const int t = width == 32 ? threadIdx.x % 32 : threadIdx.x;
-    const int64_t row = width == 32 ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-    if (row >= M) return;   // whole warps, and only where a row is a warp's
-    const int64_t base = row * K, total = M * K;
-    float x[NU][kUnit];
-    float s = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-        load_unit<T, VEC>(X, base, total, unit_first<VEC>(u, width, t), width, K, x[u], kSiteNormX);
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) s += x[u][i];
+// CTAs meant to be on an SM: about 768 threads of up to 85 registers; rows of more than 256 threads 1024 of 64
+constexpr int fwd_ctas(int threads) { return threads <= 256 ? 768 / threads : 1024 / threads; }
+// Rows ahead: what keeps about 128 KB in flight on an SM, one to three.
+template <typename T>
+constexpr int fwd_ahead(int units, int threads) {
+    const int rows = 131072 / (fwd_ctas(threads) * units * pieces<T>() * threads * 16);
+    return rows > 3 ? 3 : (rows < 1 ? 1 : rows);
+}
+
+// One row per warp (WARP: several rows a CTA) or per CTA, held in NU units a thread; the grid walks the
+// rows. THREADS is what the CTA has at most. Enough rows are on an SM at once for one row's sums (two
+// trees with a barrier each, where a row is a CTA's) to pass behind the others' work.
+template <typename T, typename W, bool VEC, bool WARP, int NU, int THREADS>
+__global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(const T* __restrict__ X, const W* __restrict__ w,
+                                                                             const W* __restrict__ b, T* __restrict__ Y,
+                                                                             float* __restrict__ mean_out, float* __restrict__ rstd_out,
+                                                                             int64_t M, int K, float eps) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(16) float buf[2][32];
+    constexpr int kDepth = fwd_ahead<T>(NU, THREADS), kRow = NU * pieces<T>() * THREADS * 16;
+    const int width = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t step = WARP ? (int64_t)gridDim.x * (THREADS / 32) : gridDim.x, stride = step * K;
+    int64_t row = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + threadIdx.x / 32 : blockIdx.x;
+    if (!WARP) {
+        if (threadIdx.x < 64) buf[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+        __syncthreads();
     }
-    const float mean = row_sum(s, width, buf) / (float)K;
-    float q = 0.0f;
+    const float inv = 1.0f / (float)K;
+    const uint32_t place = ptx::smem_u32(ring) + threadIdx.x * 16;
+    const T* in = X + row * K;              // the row that is worked on, and the next one to be copied
+    const T* from = in;
+    T* out = Y + row * K;
+    int64_t from_row = row;
+    auto ahead = [&](int slot) {
+        if (!VEC) return;
+        if (from_row < M) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-            const int first = unit_first<VEC>(u, width, t);
-            const bool in = VEC ? first < K : first + i * width < K;
-            const float d = in ? x[u][i] - mean : 0.0f;
-            x[u][i] = d;
-            q = fmaf(d, d, q);
+            for (int u = 0; u < NU; ++u) {
+                const int first = unit_first<VEC>(u, width, t);
+                const bool ok = first < K && SS1_SPAN_IN(from + first - X, kUnit, M * K, kSiteNormX);
+                unit_ahead(place + slot * kRow + u * pieces<T>() * THREADS * 16, THREADS, ok ? from + first : X, ok);
+            }
         }
-    const float rstd = 1.0f / sqrtf(row_sum(q, width, buf) / (float)K + eps);
+        from += stride;
+        from_row += step;
+        ptx::cp_async_commit();
+    };
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-        const int first = unit_first<VEC>(u, width, t);
-        float wv[kUnit], bv[kUnit];
+    for (int i = 0; i < kDepth; ++i) ahead(i);
+    for (int slot = 0; row < M; slot = slot + 1 == kDepth ? 0 : slot + 1) {     // together: all that meet at a barrier
+        [[maybe_unused]] const int64_t left = (M - row) * K;
+        F2 x[NU][4];
+        F2 s = F2::both(0.0f);
+        if (VEC) ptx::cp_async_wait<kDepth - 1>();
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) { wv[i] = 1.0f; bv[i] = 0.0f; }
-        if (w) load_unit<W, VEC>(w, 0, K, first, width, K, wv, kSiteNormW);
-        if (b) load_unit<W, VEC>(b, 0, K, first, width, K, bv, kSiteNormW);
+        for (int u = 0; u < NU; ++u) {
+            if (VEC) {
+                Raw8<T> r;
+                unit_back(ring + threadIdx.x * 16 + slot * kRow + u * pieces<T>() * THREADS * 16, THREADS, r);
+                r.get(x[u]);
+            } else {
+                load_unit<T, VEC>(in, left, unit_first<VEC>(u, width, t), width, K, x[u], 0.0f, kSiteNormX);
+            }
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[u][i] = fmaf(x[u][i] * rstd, wv[i], bv[i]);
-        store_unit<T, VEC>(Y, base, total, first, width, K, x[u], kSiteNormY);
-    }
-    if (t == 0) {
-        if (mean_out) mean_out[row] = mean;
-        if (rstd_out) rstd_out[row] = rstd;
+            for (int i = 0; i < 4; ++i) s = s + x[u][i];
+        }
+        ahead(slot);
+        const float mean = row_sum(s.lo() + s.hi(), width, buf[0]) * inv;
+        const F2 less = F2::both(-mean);
+        F2 q = F2::both(0.0f);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int first = unit_first<VEC>(u, width, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + less;
+            if (VEC) {
+                if (first >= K) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][i] = F2::both(0.0f);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[u][i] = F2::of(first + 2 * i * width < K ? x[u][i].lo() : 0.0f, first + (2 * i + 1) * width < K ? x[u][i].hi() : 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
+        }
+        const float rstd = rsqrtf(row_sum(q.lo() + q.hi(), width, buf[1]) * inv + eps);
+        const F2 by = F2::both(rstd);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int first = unit_first<VEC>(u, width, t);
+            F2 wv[4], bv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] * by;
+            if (w) {
+                load_unit<W, VEC>(w, K, first, width, K, wv, 1.0f, kSiteNormW);
+                if (b) {
+                    load_unit<W, VEC>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][i] = fma2(x[u][i], wv[i], bv[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] * wv[i];
+                }
+            } else if (b) {
+                load_unit<W, VEC>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + bv[i];
+            }
+            store_unit<T, VEC>(out, left, first, width, K, x[u], kSiteNormY);
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[row] = mean;
+            if (rstd_out) rstd_out[row] = rstd;
+        }
+        in += stride;
+        out += stride;
+        row += step;
     }
 }
 
@@ -132,18 +239,18 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* __restrict
                                                              const W* __restrict__ b, T* __restrict__ Y,
                                                              float* __restrict__ mean_out, float* __restrict__ rstd_out,
                                                              int64_t M, int64_t K, float eps) {
-    __shared__ float buf[32];
+    __shared__ __align__(16) float buf[2][32];   // 32 warps: every place is written
     const int64_t row = blockIdx.x;
     const T* x = X + row * K;
     float s = 0.0f;
     for (int64_t k = threadIdx.x; k < K; k += blockDim.x) s += SS1_IN(row * K + k, M * K, kSiteNormX) ? to_f(x[k]) : 0.0f;
-    const float mean = row_sum(s, blockDim.x, buf) / (float)K;
+    const float mean = row_sum(s, blockDim.x, buf[0]) / (float)K;
     float q = 0.0f;
     for (int64_t k = threadIdx.x; k < K; k += blockDim.x) {
         const float d = to_f(x[k]) - mean;
         q = fmaf(d, d, q);
     }
-    const float rstd = 1.0f / sqrtf(row_sum(q, blockDim.x, buf) / (float)K + eps);
+    const float rstd = 1.0f / sqrtf(row_sum(q, blockDim.x, buf[1]) / (float)K + eps);
     for (int64_t k = threadIdx.x; k < K; k += blockDim.x) {
         const float v = fmaf((to_f(x[k]) - mean) * rstd, w ? to_f(w[k]) : 1.0f, b ? to_f(b[k]) : 0.0f);
         if (SS1_IN(row * K + k, M * K, kSiteNormY)) Y[row * K + k] = from_f<T>(v);
@@ -154,13 +261,17 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* __restrict
     }
 }
 
-template <typename T, typename W, bool VEC, int NU>
+template <typename T, typename W, bool VEC, bool WARP, int NU, int THREADS>
 cudaError_t fwd_launch(const void* X, const void* w, const void* b, void* Y, float* mean, float* rstd, int64_t M, int K,
-                       float eps, int width, int threads, cudaStream_t st) {
-    const int64_t rows = width == 32 ? threads / 32 : 1;
-    const int64_t grid = (M + rows - 1) / rows;
-    norm_fwd_kernel<T, W, VEC, NU><<<(unsigned)grid, threads, 0, st>>>((const T*)X, (const W*)w, (const W*)b, (T*)Y, mean,
-                                                                      rstd, M, K, eps, width);
+                       float eps, int threads, cudaStream_t st) {
+    auto* fn = &norm_fwd_kernel<T, W, VEC, WARP, NU, THREADS>;
+    constexpr int smem = VEC ? fwd_ahead<T>(NU, THREADS) * NU * pieces<T>() * THREADS * 16 : 0;
+    if (smem > 0) {
+        const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t rows = WARP ? threads / 32 : 1, need = (M + rows - 1) / rows, most = 148 * fwd_ctas(THREADS);
+    fn<<<(unsigned)(need < most ? need : most), threads, smem, st>>>((const T*)X, (const W*)w, (const W*)b, (T*)Y, mean, rstd, M, K, eps);
     return cudaGetLastError();
 }
 
@@ -176,32 +287,41 @@ cudaError_t fwd_shape(const void* X, const void* w, const void* b, void* Y, floa
         return cudaGetLastError();
     }
     const int units = (int)((K + kUnit - 1) / kUnit);
-    // one warp a row while the row fits its registers; 8 rows a CTA
+    // one warp a row while the row fits its registers
 #define SS1_NORM_WARP(nu) \
-    if (units <= 32 * nu) return fwd_launch<T, W, VEC, nu>(X, w, b, Y, mean, rstd, M, (int)K, eps, 32, 256, st)
+    if (units <= 32 * nu) return fwd_launch<T, W, VEC, true, nu, 256>(X, w, b, Y, mean, rstd, M, (int)K, eps, 256, st)
     SS1_NORM_WARP(1);
     SS1_NORM_WARP(2);
     SS1_NORM_WARP(3);
     SS1_NORM_WARP(4);
     SS1_NORM_WARP(5);
 #undef SS1_NORM_WARP
-    const int per = units <= 1024 ? 1 : (units <= 2048 ? 2 : 4);
-    const int threads = ((units + per - 1) / per + 31) / 32 * 32;
-    if (per == 1) return fwd_launch<T, W, VEC, 1>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, threads, st);
-    if (per == 2) return fwd_launch<T, W, VEC, 2>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, threads, st);
-    return fwd_launch<T, W, VEC, 4>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, threads, st);
+    const int threads = ((units + 3) / 4 + 31) / 32 * 32;
+#define SS1_NORM_CTA(most) \
+    if (threads <= most) return fwd_launch<T, W, VEC, false, 4, most>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st)
+    SS1_NORM_CTA(64);
+    SS1_NORM_CTA(128);
+    SS1_NORM_CTA(256);
+    SS1_NORM_CTA(512);
+#undef SS1_NORM_CTA
+    return fwd_launch<T, W, VEC, false, 4, 1024>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st);
 }
 
 // ---- backward --------------------------------------------------------------------------------
 
-constexpr int64_t kBwdWidest = 1024 * kUnit;   // widest row that one CTA holds at a unit a thread
-constexpr int kBwdThreads = 512;               // threads a CTA aims at: several row groups where rows are narrow
-constexpr int kBwdCtas = 296;                  // CTAs at most (two for each of 148 SMs); each writes one partial sum
+constexpr int kBwdThreads = 640;                   // threads of a CTA at most, one CTA an SM: up to 102 registers each
+constexpr int kBwdCtas = 148;                      // CTAs at most; each writes one partial sum
+constexpr int64_t kBwdWidest = 512 * 2 * kUnit;    // widest row that a CTA holds
 
-int bwd_group_threads(int64_t K) { return (int)(((K + kUnit - 1) / kUnit + 31) / 32 * 32); }
+// Rows up to 4096 wide: a unit a thread, two rows a turn; wider ones: two units, one row.
+constexpr int64_t kBwdPairs = 512 * kUnit;
+int bwd_group_threads(int64_t K) {
+    const int64_t each = K <= kBwdPairs ? kUnit : 2 * kUnit;
+    return (int)(((K + each - 1) / each + 31) / 32 * 32);
+}
 int bwd_groups(int64_t K) {
     const int n = kBwdThreads / bwd_group_threads(K);
-    return n < 1 ? 1 : (n > 8 ? 8 : n);
+    return n > 15 ? 15 : n;                        // a named barrier each
 }
 // Rows of the partial sums [parts, 2, K].
 int64_t bwd_parts(int64_t M, int64_t K) {
@@ -210,93 +330,170 @@ int64_t bwd_parts(int64_t M, int64_t K) {
     return need < kBwdCtas ? need : kBwdCtas;
 }
 
-// Both sums over one row: within the group's warps, through `buf` (two floats a warp, two sets in
-// turn, so that one barrier a row is enough).
-__device__ __forceinline__ float2 group_sums(float a, float b, int warps, int warp, float2* buf, int bar, int width) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (warps == 1) return make_float2(a, b);
-    if (threadIdx.x % 32 == 0) buf[warp] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(width) : "memory");
-    const float2 v = (int)(threadIdx.x % 32) < warps ? buf[threadIdx.x % 32] : make_float2(0.f, 0.f);
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
-}
+// A CTA is `groups` groups of `width` threads; group g of CTA c takes ROWS rows at a time, from row
+// (c * groups + g) * ROWS in steps of the grid. A thread keeps its columns all the way: its sums of dw and
+// db stay in registers over all rows, the groups' are added in shared memory in group order, and each CTA
+// writes one partial row. A row's two sums take two trees and a barrier of its group; two rows a
+// turn share them.
+template <typename T>
+constexpr int bwd_ahead() { return sizeof(T) == 2 ? 3 : 2; }    // turns ahead: 48 or 96 KB each
 
-// A CTA is `groups` groups of `width` threads; group g of CTA c takes rows c * groups + g and so on
-// in steps of the grid. A thread keeps one unit of columns all the way: its sums of dw and db stay in
-// registers over all rows, the groups' are added in shared memory in group order, and each CTA
-// writes one partial row. The next row's loads are issued before the present row's sums.
-template <typename T, typename W, bool VEC>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* __restrict__ dY, const T* __restrict__ X,
-                                                        const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                        const W* __restrict__ w, T* __restrict__ dX,
-                                                        float* __restrict__ part, int64_t M, int K, int width, int groups) {
-    extern __shared__ float col[];                    // [2][K] where groups > 1
-    __shared__ float2 buf[2][8][32];
-    const int g = threadIdx.x / width, t = threadIdx.x % width;
-    const int first = unit_first<VEC>(0, width, t);
-    const int64_t total = M * K;
-    float wv[kUnit], sw[kUnit], sb[kUnit], x[kUnit], dy[kUnit], nx[kUnit], ndy[kUnit];
+template <typename T, typename W, bool VEC, int UNITS, int ROWS>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restrict__ dY, const T* __restrict__ X,
+                                                               const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                               const W* __restrict__ w, T* __restrict__ dX, float* __restrict__ part,
+                                                               int64_t M, int K, int width, int groups) {
+    static_assert(UNITS * ROWS == 2, "one turn's pieces");
+    extern __shared__ __align__(16) uint8_t ring[];             // the turns ahead, later [2][K] sums where groups > 1
+    __shared__ __align__(16) float4 buf[2][15][16];             // a row's two sums of each warp, for two rows
+    constexpr int kDepth = bwd_ahead<T>(), kPlace = pieces<T>() * kBwdThreads * 16, kTurn = 4 * kPlace;
+    let_next_start();
+    const int g = threadIdx.x / width, t = threadIdx.x % width, warps = width / 32, warp = t / 32;
+    for (int i = threadIdx.x; i < 2 * 15 * 16; i += blockDim.x) (&buf[0][0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    const float inv = 1.0f / (float)K;
+    const int64_t total = M * K, step = (int64_t)gridDim.x * groups * ROWS;
+    F2 sw[UNITS][4], sb[UNITS][4], wv[UNITS][4];
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) { wv[i] = 1.0f; sw[i] = 0.0f; sb[i] = 0.0f; }
-    if (w) load_unit<W, VEC>(w, 0, K, first, width, K, wv, kSiteNormW);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + g;
-    if (row < M) {
-        load_unit<T, VEC>(X, row * K, total, first, width, K, nx, kSiteNormX);
-        load_unit<T, VEC>(dY, row * K, total, first, width, K, ndy, kSiteNormX);
+    for (int u = 0; u < UNITS; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { sw[u][i] = sb[u][i] = F2::both(0.0f); wv[u][i] = F2::both(1.0f); }
+        if (w) load_unit<W, VEC>(w, K, unit_first<VEC>(u, width, t), width, K, wv[u], 0.0f, kSiteNormW);
     }
-    for (int turn = 0; row < M; row += step, turn ^= 1) {
-        const float mu = mean[row], rs = rstd[row];
+    int64_t row = ((int64_t)blockIdx.x * groups + g) * ROWS, from = row;
+    const uint32_t place = ptx::smem_u32(ring) + threadIdx.x * 16;
+    auto ahead = [&](int slot) {
+        if (!VEC) return;
+        if (from < M) {
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) { x[i] = nx[i]; dy[i] = ndy[i]; }
-        if (row + step < M) {
-            load_unit<T, VEC>(X, (row + step) * K, total, first, width, K, nx, kSiteNormX);
-            load_unit<T, VEC>(dY, (row + step) * K, total, first, width, K, ndy, kSiteNormX);
-        }
-        float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-            const bool in = VEC ? first < K : first + i * width < K;
-            const float xh = in ? (x[i] - mu) * rs : 0.0f;   // dy is 0 behind the row's end
-            sw[i] = fmaf(dy[i], xh, sw[i]);
-            sb[i] += dy[i];
-            x[i] = xh;
-            dy[i] *= wv[i];
-            a += dy[i];
-            b = fmaf(dy[i], xh, b);
-        }
-        if (!dX) continue;
-        const float2 s = group_sums(a, b, width / 32, t / 32, buf[turn][g], 1 + g, width);
-        const float ma = s.x / (float)K, mb = s.y / (float)K;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] = rs * (dy[i] - ma - x[i] * mb);
-        store_unit<T, VEC>(dX, row * K, total, first, width, K, x, kSiteNormY);
-    }
-    if (!part) return;
-    float* mine = part + (int64_t)blockIdx.x * 2 * K;
-    const int64_t parts = (int64_t)gridDim.x * 2 * K;
-    if (groups > 1) {
-        for (int k = threadIdx.x; k < 2 * K; k += blockDim.x) col[k] = 0.0f;
-        for (int turn = 0; turn < groups; ++turn) {
-            __syncthreads();
-            if (g != turn) continue;
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) {
-                const int k = VEC ? first + i : first + i * width;
-                if (k < K) { col[k] += sw[i]; col[K + k] += sb[i]; }
+            for (int e = 0; e < 2; ++e) {                       // the turn's two units: two rows', or one row's
+                const int64_t r = from + (ROWS == 2 ? e : 0);
+                const int first = unit_first<VEC>(ROWS == 2 ? 0 : e, width, t);
+                const bool ok = r < M && first < K && SS1_SPAN_IN(r * K + first, kUnit, total, kSiteNormX);
+                const int64_t at = ok ? r * K + first : 0;
+                unit_ahead(place + slot * kTurn + e * 2 * kPlace, kBwdThreads, X + at, ok);
+                unit_ahead(place + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dY + at, ok);
             }
         }
-        __syncthreads();
-        for (int k = threadIdx.x; k < 2 * K; k += blockDim.x)
-            if (SS1_IN(mine + k - part, parts, kSiteNormPart)) mine[k] = col[k];
-        return;
-    }
+        from += step;
+        ptx::cp_async_commit();
+    };
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-        const int k = VEC ? first + i : first + i * width;
-        if (k < K && SS1_SPAN_IN(mine + k - part, K + 1, parts, kSiteNormPart)) { mine[k] = sw[i]; mine[K + k] = sb[i]; }
+    for (int i = 0; i < kDepth; ++i) ahead(i);
+    float mu[ROWS], rs[ROWS], next_mu[ROWS], next_rs[ROWS];      // statistics a turn ahead; 0 behind the last row
+    auto look_up = [&](int64_t r0) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            next_mu[r] = r0 + r < M ? mean[r0 + r] : 0.0f;
+            next_rs[r] = r0 + r < M ? rstd[r0 + r] : 0.0f;
+        }
+    };
+    look_up(row);
+    for (int turn = 0, slot = 0; row < M; row += step, turn ^= 1, slot = slot + 1 == kDepth ? 0 : slot + 1) {
+        F2 x[2][4], dy[2][4];
+        if (VEC) ptx::cp_async_wait<kDepth - 1>();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (VEC) {
+                const uint8_t* p = ring + threadIdx.x * 16 + slot * kTurn + e * 2 * kPlace;
+                Raw8<T> r;
+                unit_back(p, kBwdThreads, r);
+                r.get(x[e]);
+                unit_back(p + kPlace, kBwdThreads, r);
+                r.get(dy[e]);
+            } else {
+                const int64_t r = row + (ROWS == 2 ? e : 0);
+                const int k = r < M ? K : 0;
+                const int first = unit_first<VEC>(ROWS == 2 ? 0 : e, width, t);
+                load_unit<T, VEC>(X + r * K, total - r * K, first, width, k, x[e], 0.0f, kSiteNormX);
+                load_unit<T, VEC>(dY + r * K, total - r * K, first, width, k, dy[e], 0.0f, kSiteNormX);
+            }
+        }
+        ahead(slot);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) { mu[r] = next_mu[r]; rs[r] = next_rs[r]; }
+        look_up(row + step);
+        F2 a[ROWS], b[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) a[r] = b[r] = F2::both(0.0f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = ROWS == 2 ? e : 0, u = ROWS == 2 ? 0 : e;
+            const F2 less = F2::both(-mu[r]), by = F2::both(rs[r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {     // behind the row's end dy is 0, and so is all that it is a factor of
+                const F2 xh = (x[e][i] + less) * by;
+                sw[u][i] = fma2(dy[e][i], xh, sw[u][i]);
+                sb[u][i] = sb[u][i] + dy[e][i];
+                x[e][i] = xh;
+                dy[e][i] = dy[e][i] * wv[u][i];
+                a[r] = a[r] + dy[e][i];
+                b[r] = fma2(dy[e][i], xh, b[r]);
+            }
+        }
+        if (!dX) continue;
+        float4 s = make_float4(a[0].lo() + a[0].hi(), b[0].lo() + b[0].hi(), a[ROWS - 1].lo() + a[ROWS - 1].hi(),
+                               b[ROWS - 1].lo() + b[ROWS - 1].hi());
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+            s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+            if (ROWS == 2) {
+                s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
+                s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, o);
+            }
+        }
+        if (warps > 1) {      // two buffers in turn: one barrier a turn is enough
+            if (threadIdx.x % 32 == 0) buf[turn][g][warp] = s;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(width) : "memory");
+            F2 p = F2::both(0.0f), q = p;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (k % 4 == 0 && k >= warps) break;
+                const float4 v = buf[turn][g][k];
+                p = p + F2::of(v.x, v.y);
+                if (ROWS == 2) q = q + F2::of(v.z, v.w);
+            }
+            s = make_float4(p.lo(), p.hi(), q.lo(), q.hi());
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = ROWS == 2 ? e : 0;
+            const F2 ma = F2::both(-(r ? s.z : s.x) * inv), mb = F2::both(-(r ? s.w : s.y) * inv), by = F2::both(rs[r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[e][i] = (fma2(x[e][i], mb, dy[e][i]) + ma) * by;
+            if (row + r < M)
+                store_unit<T, VEC>(dX + (row + r) * K, total - (row + r) * K, unit_first<VEC>(ROWS == 2 ? 0 : e, width, t), width, K, x[e],
+                                   kSiteNormY);
+        }
     }
+    if (!part) return;
+    float* to = part + (int64_t)blockIdx.x * 2 * K;
+    [[maybe_unused]] const int64_t parts = (int64_t)(gridDim.x - blockIdx.x) * 2 * K;
+    float* col = reinterpret_cast<float*>(ring);
+    if (groups > 1) {
+        if (VEC) ptx::cp_async_wait<0>();
+        __syncthreads();
+        for (int k = threadIdx.x; k < 2 * K; k += blockDim.x) col[k] = 0.0f;
+    }
+    for (int turn = 0; turn < groups; ++turn) {
+        if (groups > 1) __syncthreads();
+        if (g != turn) continue;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) {
+                const int first = unit_first<VEC>(u, width, t), k = VEC ? first + i : first + i * width;
+                const float vw = i % 2 ? sw[u][i / 2].hi() : sw[u][i / 2].lo(), vb = i % 2 ? sb[u][i / 2].hi() : sb[u][i / 2].lo();
+                if (k >= K) continue;
+                if (groups > 1) { col[k] += vw; col[K + k] += vb; }
+                else if (SS1_SPAN_IN(k, K + 1, parts, kSiteNormPart)) { to[k] = vw; to[K + k] = vb; }
+            }
+    }
+    if (groups == 1) return;
+    __syncthreads();
+    for (int k = threadIdx.x; k < 2 * K; k += blockDim.x)
+        if (SS1_IN(k, parts, kSiteNormPart)) to[k] = col[k];
 }
 
 // Rows wider than kBwdWidest: dX a row per CTA in two passes, and the column sums apart.
@@ -304,7 +501,7 @@ template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const T* __restrict__ dY, const T* __restrict__ X,
                                                              const float* __restrict__ mean, const float* __restrict__ rstd,
                                                              const W* __restrict__ w, T* __restrict__ dX, int64_t M, int64_t K) {
-    __shared__ float buf[32];
+    __shared__ __align__(16) float buf[2][32];   // 32 warps: every place is written
     const int64_t row = blockIdx.x;
     const float mu = mean[row], rs = rstd[row];
     float a = 0.0f, b = 0.0f;
@@ -314,8 +511,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const T* __restrict
         a += gk;
         b = fmaf(gk, in ? (to_f(X[row * K + k]) - mu) * rs : 0.0f, b);
     }
-    const float ma = row_sum(a, blockDim.x, buf) / (float)K;
-    const float mb = row_sum(b, blockDim.x, buf) / (float)K;
+    const float ma = row_sum(a, blockDim.x, buf[0]) / (float)K;
+    const float mb = row_sum(b, blockDim.x, buf[1]) / (float)K;
     for (int64_t k = threadIdx.x; k < K; k += blockDim.x) {
         if (!SS1_IN(row * K + k, M * K, kSiteNormY)) continue;
         const float gk = to_f(dY[row * K + k]) * (w ? to_f(w[k]) : 1.0f);
@@ -346,6 +543,7 @@ template <typename W>
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* __restrict__ part, W* __restrict__ dw,
                                                             W* __restrict__ db, int64_t parts, int64_t K) {
     __shared__ float acc[32][33];
+    wait_for_previous();
     const int64_t j = (int64_t)blockIdx.x * 32 + threadIdx.x;   // column of [2 K]: dw, then db
     float s = 0.0f;
     if (j < 2 * K)
@@ -360,6 +558,20 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* __restr
     else if (db) db[c - K] = from_f<W>(s);
 }
 
+template <typename T, typename W, bool VEC, int UNITS, int ROWS>
+cudaError_t bwd_rows(const void* dY, const void* X, const float* mean, const float* rstd, const void* w, void* dX, float* part, int64_t M,
+                     int K, int ctas, cudaStream_t st) {
+    auto* fn = &norm_bwd_kernel<T, W, VEC, UNITS, ROWS>;
+    const int width = bwd_group_threads(K), groups = bwd_groups(K);
+    // the turns ahead, and the groups' sums over them: K <= 8 * kBwdThreads / 2 where there are several groups
+    constexpr int most_sums = 2 * (kBwdThreads / 2) * kUnit * (int)sizeof(float);
+    constexpr int turns = VEC ? bwd_ahead<T>() * 4 * pieces<T>() * kBwdThreads * 16 : 0, smem = turns > most_sums ? turns : most_sums;
+    const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), smem);
+    if (e != cudaSuccess) return e;
+    fn<<<(unsigned)ctas, width * groups, smem, st>>>((const T*)dY, (const T*)X, mean, rstd, (const W*)w, (T*)dX, part, M, K, width, groups);
+    return cudaGetLastError();
+}
+
 template <typename T, typename W, bool VEC>
 cudaError_t bwd_shape(const void* dY, const void* X, const float* mean, const float* rstd, const void* w, void* dX, void* dw,
                       void* db, int64_t M, int64_t K, float* ws, cudaStream_t st) {
@@ -371,15 +583,14 @@ cudaError_t bwd_shape(const void* dY, const void* X, const float* mean, const fl
         if (part) norm_bwd_columns_kernel<T><<<dim3((unsigned)((K + 255) / 256), (unsigned)parts), 256, 0, st>>>(
             (const T*)dY, (const T*)X, mean, rstd, part, M, K);
     } else if (M > 0) {
-        const int width = bwd_group_threads(K), groups = bwd_groups(K);
-        const size_t smem = groups > 1 ? 2 * (size_t)K * sizeof(float) : 0;   // K <= 2048 there: 16 KB
-        norm_bwd_kernel<T, W, VEC><<<(unsigned)parts, width * groups, smem, st>>>(
-            (const T*)dY, (const T*)X, mean, rstd, (const W*)w, (T*)dX, part, M, (int)K, width, groups);
+        const cudaError_t e = K <= kBwdPairs ? bwd_rows<T, W, VEC, 1, 2>(dY, X, mean, rstd, w, dX, part, M, (int)K, (int)parts, st)
+                                             : bwd_rows<T, W, VEC, 2, 1>(dY, X, mean, rstd, w, dX, part, M, (int)K, (int)parts, st);
+        if (e != cudaSuccess) return e;
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(dw || db)) return e;
-    norm_bwd_sum_kernel<W><<<(unsigned)((2 * K + 31) / 32), dim3(32, 32), 0, st>>>(part, (W*)dw, (W*)db, parts, K);
-    return cudaGetLastError();
+    return launch_dependent(&norm_bwd_sum_kernel<W>, dim3((unsigned)((2 * K + 31) / 32)), dim3(32, 32), 0, st, (const float*)part, (W*)dw,
+                            (W*)db, parts, K);
 }
 
 bool sizes_ok(int64_t M, int64_t K, int dtype, int w_dtype) {

@@ -31,6 +31,35 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Two floats in one 64-bit register pair: sm_100's packed float32 operations do both at once, each
+// rounded as the single one is.
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ static F2 of(float lo, float hi) {
+        F2 r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+        return r;
+    }
+    __device__ __forceinline__ static F2 both(float x) { return of(x, x); }
+    __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Eight consecutive elements, 16-byte aligned, as they lie in memory (bf16: one 16-byte word,
 // float: two).
 template <typename T>
@@ -49,6 +78,20 @@ struct Raw8<__nv_bfloat16> {
             f[2 * i] = __uint_as_float(w[i] << 16);
             f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
+    }
+    __device__ __forceinline__ void get(F2 (&f)[4]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = F2::of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void set(const F2 (&f)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[i].lo(), f[i].hi());
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        a = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ void set(const float (&f)[8]) {
         uint32_t w[4];
@@ -79,6 +122,13 @@ struct Raw8<float> {
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void get(F2 (&f)[4]) const {
+        f[0] = F2::of(a.x, a.y); f[1] = F2::of(a.z, a.w); f[2] = F2::of(b.x, b.y); f[3] = F2::of(b.z, b.w);
+    }
+    __device__ __forceinline__ void set(const F2 (&f)[4]) {
+        a = make_float4(f[0].lo(), f[0].hi(), f[1].lo(), f[1].hi());
+        b = make_float4(f[2].lo(), f[2].hi(), f[3].lo(), f[3].hi());
     }
     __device__ __forceinline__ void set(const float (&f)[8]) {
         a = make_float4(f[0], f[1], f[2], f[3]);
