@@ -59,91 +59,176 @@ struct Factors {
 };
 constexpr int kFactors = sizeof(Factors) / sizeof(float);
 
-// Eight elements from `at` on, `n` of them inside the tensor; 0 in the others.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t at, int n, bool vec, float (&f)[8]) {
-    if (vec && n == 8) {
+// a * b rounded by itself: with `none` = -0, a * b + none has its value and its sign. `none` is a kernel
+// parameter, because the assembler turns a constant -0 back into a product and joins that with the
+// sum that follows.
+__device__ __forceinline__ F2 times(F2 a, F2 b, F2 none) { return fma2(a, b, none); }
+
+// Eight elements at `p`. WHOLE: all inside the tensor and on vector boundaries; else the first `n`, one at a
+// time (0 in the others).
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void load8(const T* p, int n, F2 (&f)[4]) {
+    if (WHOLE) {
         Raw8<T> r;
-        r.load_once(p + at);
+        r.load_once(p);
         r.get(f);
     } else {
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f(p[at + i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = F2::of(v[2 * i], v[2 * i + 1]);
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t at, int n, bool vec, const float (&f)[8]) {
-    if (vec && n == 8) {
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store8(T* p, int n, const F2 (&f)[4]) {
+    if (WHOLE) {
         Raw8<T> r;
         r.set(f);
-        r.store(p + at);
+        r.store(p);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[at + i] = from_f<T>(f[i]);
+            if (i < n) p[i] = from_f<T>(i % 2 ? f[i / 2].hi() : f[i / 2].lo());
     }
 }
 
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t at, int n, bool vec) {
-    if (vec && n == 8) return __ldcs(reinterpret_cast<const uint2*>(p + at));
+template <bool WHOLE>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int n) {
+    if (WHOLE) return __ldcs(reinterpret_cast<const uint2*>(p));
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (i < n) w[i / 4] |= (uint32_t)p[at + i] << (8 * (i % 4));
+        if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t at, int n, bool vec, uint2 c) {
-    if (vec && n == 8) {
-        *reinterpret_cast<uint2*>(p + at) = c;
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint2 c) {
+    if (WHOLE) {
+        *reinterpret_cast<uint2*>(p) = c;
         return;
     }
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (i < n) p[at + i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+        if (i < n) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
 }
 
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
+__device__ __forceinline__ void decode8(uint2 c, float scale, F2 (&f)[4]) {
     const uint32_t w[2] = {c.x, c.y};
+    const F2 by = F2::both(scale);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2)));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        const float2 x = __half22float2(__half2(h));
-        f[2 * i] = __fmul_rn(x.x, scale);
-        f[2 * i + 1] = __fmul_rn(x.y, scale);
+        const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+        f[i] = F2::of(x.x, x.y) * by;
     }
 }
 
-// The block's scale from the largest magnitude (the bits of its absolute value) over the warp.
-__device__ __forceinline__ float block_scale(const float (&f)[8]) {
-    uint32_t top = 0;
+// The block's scale from its largest magnitude over the warp; a NaN does not count.
+__device__ __forceinline__ float block_scale(const F2 (&f)[4]) {
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    // top = 1.f * 2^ex: 448 is 1.75 * 2^8
+    for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(f[i].lo()), fabsf(f[i].hi())));
+    // magnitudes order like their bits: top = 1.f * 2^ex, and 448 is 1.75 * 2^8
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
     const int ex = (int)(top >> 23) - 127;
     const int e = (top & 0x7FFFFFu) <= 0x600000u ? ex - 8 : ex - 7;
     return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float scale) {
+__device__ __forceinline__ uint2 encode8(const F2 (&f)[4], float scale) {
     // 1 / scale, exactly: scale = 2^e with -126 <= e <= 121
-    const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
+    const F2 by = F2::both(__uint_as_float((254u << 23) - __float_as_uint(scale)));
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 x = make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv));
-        w[i / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3) << (16 * (i % 2));
+        const F2 x = f[i] * by;   // exact but for results below 2^-126
+        w[i / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.lo(), x.hi()), __NV_SATFINITE, __NV_E4M3) << (16 * (i % 2));
     }
     return make_uint2(w[0], w[1]);
 }
 
+// Eight elements of one lane: `at` in the tensor, `block` their block, whose 32 lanes come here together.
+template <int BITS, bool WHOLE>
+__device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Factors& f, F2 none, int64_t at, int n, int64_t block, int lane) {
+    F2 g[4], p[4], m[4], v[4], root[4];
+    uint2 mc, vc;
+    float ms, vs;
+    if (flags & kGradBf16) load8<__nv_bfloat16, WHOLE>((const __nv_bfloat16*)t.g + at, n, g);
+    else load8<float, WHOLE>((const float*)t.g + at, n, g);
+    if (t.master) load8<float, WHOLE>(t.master + at, n, p);
+    else if (flags & kParamBf16) load8<__nv_bfloat16, WHOLE>((const __nv_bfloat16*)t.p + at, n, p);
+    else load8<float, WHOLE>((const float*)t.p + at, n, p);
+    if (BITS == 32) {
+        load8<float, WHOLE>((const float*)t.m + at, n, m);
+        load8<float, WHOLE>((const float*)t.v + at, n, v);
+    } else {
+        mc = load_codes<WHOLE>((const uint8_t*)t.m + at, n);
+        vc = load_codes<WHOLE>((const uint8_t*)t.v + at, n);
+        ms = t.m_scale[block];
+        vs = t.v_scale[block];
+        decode8(mc, ms, m);
+        decode8(vc, vs, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = times(v[i], v[i], none);
+    }
+    const F2 beta1 = F2::both(f.beta1), rest1 = F2::both(f.rest1), beta2 = F2::both(f.beta2), rest2 = F2::both(f.rest2);
+    const F2 scale = F2::both(f.grad), eps = F2::both(f.eps), by_root = F2::both(f.root), keep = F2::both(f.keep), back = F2::both(-f.step);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const F2 gi = times(g[i], scale, none);
+        m[i] = times(m[i], beta1, none) + times(gi, rest1, none);
+        v[i] = times(v[i], beta2, none) + times(times(gi, gi, none), rest2, none);
+        root[i] = F2::of(__fsqrt_rn(v[i].lo()), __fsqrt_rn(v[i].hi()));
+        const F2 den = times(root[i], by_root, none) + eps;
+        const F2 q = F2::of(__fdiv_rn(m[i].lo(), den.lo()), __fdiv_rn(m[i].hi(), den.hi()));
+        p[i] = times(p[i], keep, none) + times(q, back, none);     // a - b is a + (-b)
+    }
+    if (t.master) store8<float, WHOLE>(t.master + at, n, p);
+    if (flags & kParamBf16) store8<__nv_bfloat16, WHOLE>((__nv_bfloat16*)t.p + at, n, p);
+    else store8<float, WHOLE>((float*)t.p + at, n, p);
+    if (BITS == 32) {
+        store8<float, WHOLE>((float*)t.m + at, n, m);
+        store8<float, WHOLE>((float*)t.v + at, n, v);
+        return;
+    }
+    if (!WHOLE) {   // what lies behind the tensor's end takes no part in the block's maximum
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = F2::of(2 * i < n ? m[i].lo() : 0.0f, 2 * i + 1 < n ? m[i].hi() : 0.0f);
+            root[i] = F2::of(2 * i < n ? root[i].lo() : 0.0f, 2 * i + 1 < n ? root[i].hi() : 0.0f);
+        }
+    }
+    ms = block_scale(m);
+    vs = block_scale(root);
+    mc = encode8(m, ms);
+    vc = encode8(root, vs);
+    // a positive root that rounded to code 0 takes code 1; most words have no zero byte
+    uint32_t w[2] = {vc.x, vc.y};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if ((w[h] - 0x01010101u) & ~w[h] & 0x80808080u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float r = i % 2 ? root[2 * h + i / 2].hi() : root[2 * h + i / 2].lo();
+                if (r > 0.0f && !((w[h] >> (8 * i)) & 0xFFu)) w[h] |= 1u << (8 * i);
+            }
+        }
+    store_codes<WHOLE>((uint8_t*)t.m + at, n, mc);
+    store_codes<WHOLE>((uint8_t*)t.v + at, n, make_uint2(w[0], w[1]));
+    if (lane == 0 && SS1_IN(block, (t.n + kBlock - 1) / kBlock, kSiteAdamScale)) {
+        t.m_scale[block] = ms;
+        t.v_scale[block] = vs;
+    }
+}
+
 template <int N, int BITS>
 __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
-                                                            const float* __restrict__ device) {
+                                                            const float* __restrict__ device, float minus_zero) {
+    const F2 none = F2::both(minus_zero);
     Factors f = host;
     if (device) {
         float* to = reinterpret_cast<float*>(&f);
@@ -157,64 +242,19 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
         if (table.first[mid] <= (int)blockIdx.x) lo = mid;
         else hi = mid - 1;
     }
-    const Entry& t = table.t[lo];
+    const Entry t = table.t[lo];
     const uint32_t flags = table.flags[lo];
-    const bool vec = flags & kAligned;
     const int64_t start = (int64_t)((int)blockIdx.x - table.first[lo]) * kChunk;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    for (int64_t block = start / kBlock + warp; block < (start + kChunk) / kBlock && block * kBlock < t.n; block += kWarps) {
-        const int64_t at = block * kBlock + lane * 8;
-        const int64_t left = t.n - at;
-        int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-        if (n > 0 && !SS1_SPAN_IN(at, n, t.n, kSiteAdamTensor)) n = 0;
-        float g[8], p[8], m[8], v[8];
-        if (flags & kGradBf16) load8((const __nv_bfloat16*)t.g, at, n, vec, g);
-        else load8((const float*)t.g, at, n, vec, g);
-        if (t.master) load8((const float*)t.master, at, n, vec, p);
-        else if (flags & kParamBf16) load8((const __nv_bfloat16*)t.p, at, n, vec, p);
-        else load8((const float*)t.p, at, n, vec, p);
-        if (BITS == 32) {
-            load8((const float*)t.m, at, n, vec, m);
-            load8((const float*)t.v, at, n, vec, v);
+#pragma unroll 1
+    for (int k = warp; k < kChunk / kBlock; k += kWarps) {
+        const int64_t block = start / kBlock + k, at = block * kBlock + lane * 8;
+        if (block * kBlock >= t.n) break;
+        if ((flags & kAligned) && (block + 1) * kBlock <= t.n && SS1_SPAN_IN(at, 8, t.n, kSiteAdamTensor)) {
+            update8<BITS, true>(t, flags, f, none, at, 8, block, lane);
         } else {
-            const uint2 mc = load_codes((const uint8_t*)t.m, at, n, vec), vc = load_codes((const uint8_t*)t.v, at, n, vec);
-            decode8(mc, t.m_scale[block], m);
-            decode8(vc, t.v_scale[block], v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-        }
-        float root[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gi = __fmul_rn(g[i], f.grad);
-            m[i] = __fadd_rn(__fmul_rn(m[i], f.beta1), __fmul_rn(gi, f.rest1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], f.beta2), __fmul_rn(__fmul_rn(gi, gi), f.rest2));
-            root[i] = __fsqrt_rn(v[i]);
-            const float den = __fadd_rn(__fmul_rn(root[i], f.root), f.eps);
-            p[i] = __fsub_rn(__fmul_rn(p[i], f.keep), __fmul_rn(__fdiv_rn(m[i], den), f.step));
-        }
-        if (t.master) store8(t.master, at, n, vec, p);
-        if (flags & kParamBf16) store8((__nv_bfloat16*)t.p, at, n, vec, p);
-        else store8((float*)t.p, at, n, vec, p);
-        if (BITS == 32) {
-            store8((float*)t.m, at, n, vec, m);
-            store8((float*)t.v, at, n, vec, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)   // lanes behind the tensor's end take no part in the block's maximum
-                if (i >= n) m[i] = root[i] = 0.0f;
-            const float ms = block_scale(m), vs = block_scale(root);
-            uint2 mc = encode8(m, ms), vc = encode8(root, vs);
-            uint32_t w[2] = {vc.x, vc.y};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (root[i] > 0.0f && !((w[i / 4] >> (8 * (i % 4))) & 0xFFu)) w[i / 4] |= 1u << (8 * (i % 4));
-            store_codes((uint8_t*)t.m, at, n, vec, mc);
-            store_codes((uint8_t*)t.v, at, n, vec, make_uint2(w[0], w[1]));
-            if (lane == 0 && SS1_IN(block, (t.n + kBlock - 1) / kBlock, kSiteAdamScale)) {
-                t.m_scale[block] = ms;
-                t.v_scale[block] = vs;
-            }
+            const int64_t left = t.n - at;
+            update8<BITS, false>(t, flags, f, none, left > 0 ? at : 0, left >= 8 ? 8 : (left > 0 ? (int)left : 0), block, lane);
         }
     }
 }
@@ -222,7 +262,7 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
 template <int N>
 cudaError_t launch(const ss1_adamw_tensor* tensors, int64_t count, int bits, const Factors& f,
                    const float* device, cudaStream_t st) {
-    static_assert(sizeof(Table<N>) + sizeof(Factors) + 16 <= 32764, "kernel parameters");
+    static_assert(sizeof(Table<N>) + sizeof(Factors) + 24 <= 32764, "kernel parameters");
     Table<N> table;
     table.count = 0;
     int64_t chunks = 0;
@@ -240,8 +280,8 @@ cudaError_t launch(const ss1_adamw_tensor* tensors, int64_t count, int bits, con
         chunks += (t.numel + kChunk - 1) / kChunk;
     }
     if (table.count == 0) return cudaSuccess;
-    if (bits == 32) adamw_kernel<N, 32><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device);
-    else adamw_kernel<N, 8><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device);
+    if (bits == 32) adamw_kernel<N, 32><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device, -0.0f);
+    else adamw_kernel<N, 8><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device, -0.0f);
     return cudaGetLastError();
 }
 

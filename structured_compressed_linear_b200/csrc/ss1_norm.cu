@@ -13,6 +13,8 @@
 #include "ss1_ops.cuh"
 #include "ptx_sm100.cuh"
 
+#include <string.h>
+
 namespace ss1 {
 namespace {
 
@@ -69,25 +71,55 @@ __device__ __forceinline__ void store_unit(T* __restrict__ p, [[maybe_unused]] i
     }
 }
 
-// Rows on their way (vector form): every thread copies the units that it will work on into places of its own
+// Rows on their way: every thread copies the units that it will work on into places of its own
 // in shared memory, some rows ahead, and reads them back itself. So the bytes in flight cost no
-// registers, and a thread waits for its own copies only, without a barrier. A piece is 16 bytes a
-// thread, threads side by side.
+// registers, and a thread waits for its own copies only, without a barrier. Pieces are 16 bytes a
+// thread (vector rows) or 4 (scalar rows of float), threads side by side. Scalar rows of bf16 have none:
+// no copy is as small as an element, and those rows are loaded when their turn comes.
 template <typename T>
-constexpr int pieces() { return kUnit * (int)sizeof(T) / 16; }   // 16-byte pieces of a unit
+constexpr int unit_bytes() { return kUnit * (int)sizeof(T); }
+template <typename T, bool VEC>
+constexpr bool in_ring() { return VEC || sizeof(T) == 4; }
 
-template <typename T>
-__device__ __forceinline__ void unit_ahead(uint32_t place, int threads, const T* p, bool ok) {
+// `first` as unit_first gives it, from the start of the row at `p`; nothing is read where the row is not `ok`, or behind
+// its end (zeros instead). FULL: every unit lies inside the row.
+template <typename T, bool VEC, bool FULL>
+__device__ __forceinline__ void unit_ahead(uint32_t ring, int threads, const T* p, [[maybe_unused]] int64_t left, int first, int width, int K,
+                                           bool ok, const T* any, int site) {
+    if (VEC) {
+        const bool in = ok && (FULL || first < K) && SS1_SPAN_IN(first, kUnit, left, site);
+        const T* from = in ? p + first : any;
 #pragma unroll
-    for (int i = 0; i < pieces<T>(); ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place + i * threads * 16), "l"(p + i * (16 / sizeof(T))),
-                     "r"(ok ? 16 : 0)
-                     : "memory");
+        for (int i = 0; i < unit_bytes<T>() / 16; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + (i * threads + threadIdx.x) * 16),
+                         "l"(from + i * (16 / sizeof(T))), "r"(in ? 16 : 0)
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            const int k = first + i * width;
+            const bool in = ok && k < K && SS1_IN(k, left, site);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + (i * threads + threadIdx.x) * 4),
+                         "l"(in ? p + k : any), "r"(in ? 4 : 0)
+                         : "memory");
+        }
+    }
 }
-__device__ __forceinline__ void unit_back(const uint8_t* place, int, Raw8<__nv_bfloat16>& r) { r.a = *reinterpret_cast<const uint4*>(place); }
-__device__ __forceinline__ void unit_back(const uint8_t* place, int threads, Raw8<float>& r) {
-    r.a = *reinterpret_cast<const float4*>(place);
-    r.b = *reinterpret_cast<const float4*>(place + threads * 16);
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void unit_back(const uint8_t* ring, int threads, F2 (&f)[4]) {
+    if (VEC) {
+        uint4 v[unit_bytes<T>() / 16];
+#pragma unroll
+        for (int i = 0; i < unit_bytes<T>() / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(ring + (i * threads + threadIdx.x) * 16);
+        Raw8<T> r;
+        memcpy(&r, v, sizeof r);
+        r.get(f);
+    } else {
+        const float* v = reinterpret_cast<const float*>(ring) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = F2::of(v[2 * i * threads], v[(2 * i + 1) * threads]);
+    }
 }
 
 // Sum over the `width` threads of a row (one warp, or all warps of the CTA), the same in every
@@ -114,43 +146,40 @@ constexpr int fwd_ctas(int threads) { return threads <= 256 ? 768 / threads : 10
 // Rows ahead: what keeps about 128 KB in flight on an SM, one to three.
 template <typename T>
 constexpr int fwd_ahead(int units, int threads) {
-    const int rows = 131072 / (fwd_ctas(threads) * units * pieces<T>() * threads * 16);
+    const int rows = 131072 / (fwd_ctas(threads) * units * unit_bytes<T>() * threads);
     return rows > 3 ? 3 : (rows < 1 ? 1 : rows);
 }
 
 // One row per warp (WARP: several rows a CTA) or per CTA, held in NU units a thread; the grid walks the
 // rows. THREADS is what the CTA has at most. Enough rows are on an SM at once for one row's sums (two
-// trees with a barrier each, where a row is a CTA's) to pass behind the others' work.
-template <typename T, typename W, bool VEC, bool WARP, int NU, int THREADS>
+// trees with a barrier each, where a row is a CTA's) to pass behind the others' work. What is left to
+// bound it is issue slots: so sums and products go in pairs, FULL rows (all units inside) carry no
+// predicates, and where warps share a CTA the weights lie converted in shared memory.
+template <typename T, typename W, bool VEC, bool WARP, bool FULL, int NU, int THREADS>
 __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(const T* __restrict__ X, const W* __restrict__ w,
                                                                              const W* __restrict__ b, T* __restrict__ Y,
                                                                              float* __restrict__ mean_out, float* __restrict__ rstd_out,
                                                                              int64_t M, int K, float eps) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float buf[2][32];
-    constexpr int kDepth = fwd_ahead<T>(NU, THREADS), kRow = NU * pieces<T>() * THREADS * 16;
+    constexpr bool kRing = in_ring<T, VEC>(), kShared = WARP && VEC;
+    constexpr int kDepth = fwd_ahead<T>(NU, THREADS), kPlace = unit_bytes<T>() * THREADS, kRow = NU * kPlace;
+    __shared__ __align__(16) float weights[kShared ? 2 : 1][kShared ? NU * 2 : 1][kShared ? 128 : 4];   // [w, b][half unit][lane * 4]
     const int width = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x % 32 : threadIdx.x;
     const int64_t step = WARP ? (int64_t)gridDim.x * (THREADS / 32) : gridDim.x, stride = step * K;
     int64_t row = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + threadIdx.x / 32 : blockIdx.x;
-    if (!WARP) {
-        if (threadIdx.x < 64) buf[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
-        __syncthreads();
-    }
-    const float inv = 1.0f / (float)K;
-    const uint32_t place = ptx::smem_u32(ring) + threadIdx.x * 16;
+    const uint32_t place = ptx::smem_u32(ring);
     const T* in = X + row * K;              // the row that is worked on, and the next one to be copied
     const T* from = in;
     T* out = Y + row * K;
     int64_t from_row = row;
     auto ahead = [&](int slot) {
-        if (!VEC) return;
+        if (!kRing) return;
         if (from_row < M) {
 #pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const int first = unit_first<VEC>(u, width, t);
-                const bool ok = first < K && SS1_SPAN_IN(from + first - X, kUnit, M * K, kSiteNormX);
-                unit_ahead(place + slot * kRow + u * pieces<T>() * THREADS * 16, THREADS, ok ? from + first : X, ok);
-            }
+            for (int u = 0; u < NU; ++u)
+                unit_ahead<T, VEC, FULL>(place + slot * kRow + u * kPlace, THREADS, from, (M - from_row) * K, unit_first<VEC>(u, width, t),
+                                         width, K, true, X, kSiteNormX);
         }
         from += stride;
         from_row += step;
@@ -158,17 +187,28 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
     };
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) ahead(i);
+    if (kShared) {
+        for (int i = threadIdx.x; i < NU * 256; i += THREADS) {      // element i of the row: unit, lane, half, place in the half
+            const int u = i / 256, l = i / 8 % 32, h = i / 4 % 2;
+            weights[0][u * 2 + h][l * 4 + i % 4] = w && i < K ? to_f(w[i]) : 1.0f;
+            weights[kShared][u * 2 + h][l * 4 + i % 4] = b && i < K ? to_f(b[i]) : 0.0f;
+        }
+        __syncthreads();
+    }
+    if (!WARP) {
+        if (threadIdx.x < 64) buf[threadIdx.x / 32][threadIdx.x % 32] = 0.0f;
+        __syncthreads();
+    }
+    const float inv = 1.0f / (float)K;
     for (int slot = 0; row < M; slot = slot + 1 == kDepth ? 0 : slot + 1) {     // together: all that meet at a barrier
         [[maybe_unused]] const int64_t left = (M - row) * K;
         F2 x[NU][4];
         F2 s = F2::both(0.0f);
-        if (VEC) ptx::cp_async_wait<kDepth - 1>();
+        if (kRing) ptx::cp_async_wait<kDepth - 1>();
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            if (VEC) {
-                Raw8<T> r;
-                unit_back(ring + threadIdx.x * 16 + slot * kRow + u * pieces<T>() * THREADS * 16, THREADS, r);
-                r.get(x[u]);
+            if (kRing) {
+                unit_back<T, VEC>(ring + slot * kRow + u * kPlace, THREADS, x[u]);
             } else {
                 load_unit<T, VEC>(in, left, unit_first<VEC>(u, width, t), width, K, x[u], 0.0f, kSiteNormX);
             }
@@ -185,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + less;
             if (VEC) {
-                if (first >= K) {
+                if (!FULL && first >= K) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[u][i] = F2::both(0.0f);
                 }
@@ -205,7 +245,15 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
             F2 wv[4], bv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] * by;
-            if (w) {
+            if (kShared) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 wh = *reinterpret_cast<const float4*>(&weights[0][u * 2 + h][t * 4]);
+                    const float4 bh = *reinterpret_cast<const float4*>(&weights[kShared][u * 2 + h][t * 4]);
+                    x[u][2 * h] = fma2(x[u][2 * h], F2::of(wh.x, wh.y), F2::of(bh.x, bh.y));
+                    x[u][2 * h + 1] = fma2(x[u][2 * h + 1], F2::of(wh.z, wh.w), F2::of(bh.z, bh.w));
+                }
+            } else if (w) {
                 load_unit<W, VEC>(w, K, first, width, K, wv, 1.0f, kSiteNormW);
                 if (b) {
                     load_unit<W, VEC>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
@@ -220,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + bv[i];
             }
-            store_unit<T, VEC>(out, left, first, width, K, x[u], kSiteNormY);
+            store_unit<T, VEC>(out, left, first, width, FULL ? 1 << 30 : K, x[u], kSiteNormY);
         }
         if (t == 0) {
             if (mean_out) mean_out[row] = mean;
@@ -261,11 +309,11 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* __restrict
     }
 }
 
-template <typename T, typename W, bool VEC, bool WARP, int NU, int THREADS>
+template <typename T, typename W, bool VEC, bool WARP, bool FULL, int NU, int THREADS>
 cudaError_t fwd_launch(const void* X, const void* w, const void* b, void* Y, float* mean, float* rstd, int64_t M, int K,
                        float eps, int threads, cudaStream_t st) {
-    auto* fn = &norm_fwd_kernel<T, W, VEC, WARP, NU, THREADS>;
-    constexpr int smem = VEC ? fwd_ahead<T>(NU, THREADS) * NU * pieces<T>() * THREADS * 16 : 0;
+    auto* fn = &norm_fwd_kernel<T, W, VEC, WARP, FULL, NU, THREADS>;
+    constexpr int smem = in_ring<T, VEC>() ? fwd_ahead<T>(NU, THREADS) * NU * unit_bytes<T>() * THREADS : 0;
     if (smem > 0) {
         const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), smem);
         if (e != cudaSuccess) return e;
@@ -289,7 +337,8 @@ cudaError_t fwd_shape(const void* X, const void* w, const void* b, void* Y, floa
     const int units = (int)((K + kUnit - 1) / kUnit);
     // one warp a row while the row fits its registers
 #define SS1_NORM_WARP(nu) \
-    if (units <= 32 * nu) return fwd_launch<T, W, VEC, true, nu, 256>(X, w, b, Y, mean, rstd, M, (int)K, eps, 256, st)
+    if (VEC && units == 32 * nu) return fwd_launch<T, W, VEC, true, VEC, nu, 256>(X, w, b, Y, mean, rstd, M, (int)K, eps, 256, st); \
+    if (units <= 32 * nu) return fwd_launch<T, W, VEC, true, false, nu, 256>(X, w, b, Y, mean, rstd, M, (int)K, eps, 256, st)
     SS1_NORM_WARP(1);
     SS1_NORM_WARP(2);
     SS1_NORM_WARP(3);
@@ -298,13 +347,15 @@ cudaError_t fwd_shape(const void* X, const void* w, const void* b, void* Y, floa
 #undef SS1_NORM_WARP
     const int threads = ((units + 3) / 4 + 31) / 32 * 32;
 #define SS1_NORM_CTA(most) \
-    if (threads <= most) return fwd_launch<T, W, VEC, false, 4, most>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st)
+    if (VEC && units == 4 * threads && threads <= most) \
+        return fwd_launch<T, W, VEC, false, VEC, 4, most>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st); \
+    if (threads <= most) return fwd_launch<T, W, VEC, false, false, 4, most>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st)
     SS1_NORM_CTA(64);
     SS1_NORM_CTA(128);
     SS1_NORM_CTA(256);
     SS1_NORM_CTA(512);
 #undef SS1_NORM_CTA
-    return fwd_launch<T, W, VEC, false, 4, 1024>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st);
+    return fwd_launch<T, W, VEC, false, false, 4, 1024>(X, w, b, Y, mean, rstd, M, (int)K, eps, threads, st);
 }
 
 // ---- backward --------------------------------------------------------------------------------
@@ -332,7 +383,7 @@ int64_t bwd_parts(int64_t M, int64_t K) {
 
 // A CTA is `groups` groups of `width` threads; group g of CTA c takes ROWS rows at a time, from row
 // (c * groups + g) * ROWS in steps of the grid. A thread keeps its columns all the way: its sums of dw and
-// db stay in registers over all rows, the groups' are added in shared memory in group order, and each CTA
+// db stay in registers over all rows, the groups' are added through shared memory in group order, and each CTA
 // writes one partial row. A row's two sums take two trees and a barrier of its group; two rows a
 // turn share them.
 template <typename T>
@@ -344,9 +395,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
                                                                const W* __restrict__ w, T* __restrict__ dX, float* __restrict__ part,
                                                                int64_t M, int K, int width, int groups) {
     static_assert(UNITS * ROWS == 2, "one turn's pieces");
-    extern __shared__ __align__(16) uint8_t ring[];             // the turns ahead, later [2][K] sums where groups > 1
+    extern __shared__ __align__(16) uint8_t ring[];             // the turns ahead, later [groups][2][K] sums
     __shared__ __align__(16) float4 buf[2][15][16];             // a row's two sums of each warp, for two rows
-    constexpr int kDepth = bwd_ahead<T>(), kPlace = pieces<T>() * kBwdThreads * 16, kTurn = 4 * kPlace;
+    constexpr bool kRing = in_ring<T, VEC>();
+    constexpr int kDepth = bwd_ahead<T>(), kPlace = unit_bytes<T>() * kBwdThreads, kTurn = 4 * kPlace;
     let_next_start();
     const int g = threadIdx.x / width, t = threadIdx.x % width, warps = width / 32, warp = t / 32;
     for (int i = threadIdx.x; i < 2 * 15 * 16; i += blockDim.x) (&buf[0][0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -361,18 +413,18 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
         if (w) load_unit<W, VEC>(w, K, unit_first<VEC>(u, width, t), width, K, wv[u], 0.0f, kSiteNormW);
     }
     int64_t row = ((int64_t)blockIdx.x * groups + g) * ROWS, from = row;
-    const uint32_t place = ptx::smem_u32(ring) + threadIdx.x * 16;
+    const uint32_t place = ptx::smem_u32(ring);
     auto ahead = [&](int slot) {
-        if (!VEC) return;
+        if (!kRing) return;
         if (from < M) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {                       // the turn's two units: two rows', or one row's
-                const int64_t r = from + (ROWS == 2 ? e : 0);
+                const int64_t r = from + (ROWS == 2 ? e : 0), at = r * K;
                 const int first = unit_first<VEC>(ROWS == 2 ? 0 : e, width, t);
-                const bool ok = r < M && first < K && SS1_SPAN_IN(r * K + first, kUnit, total, kSiteNormX);
-                const int64_t at = ok ? r * K + first : 0;
-                unit_ahead(place + slot * kTurn + e * 2 * kPlace, kBwdThreads, X + at, ok);
-                unit_ahead(place + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dY + at, ok);
+                unit_ahead<T, VEC, false>(place + slot * kTurn + e * 2 * kPlace, kBwdThreads, X + at, total - at, first, width, K, r < M, X,
+                                          kSiteNormX);
+                unit_ahead<T, VEC, false>(place + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dY + at, total - at, first, width, K,
+                                          r < M, dY, kSiteNormX);
             }
         }
         from += step;
@@ -391,16 +443,12 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
     look_up(row);
     for (int turn = 0, slot = 0; row < M; row += step, turn ^= 1, slot = slot + 1 == kDepth ? 0 : slot + 1) {
         F2 x[2][4], dy[2][4];
-        if (VEC) ptx::cp_async_wait<kDepth - 1>();
+        if (kRing) ptx::cp_async_wait<kDepth - 1>();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if (VEC) {
-                const uint8_t* p = ring + threadIdx.x * 16 + slot * kTurn + e * 2 * kPlace;
-                Raw8<T> r;
-                unit_back(p, kBwdThreads, r);
-                r.get(x[e]);
-                unit_back(p + kPlace, kBwdThreads, r);
-                r.get(dy[e]);
+            if (kRing) {
+                unit_back<T, VEC>(ring + slot * kTurn + e * 2 * kPlace, kBwdThreads, x[e]);
+                unit_back<T, VEC>(ring + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dy[e]);
             } else {
                 const int64_t r = row + (ROWS == 2 ? e : 0);
                 const int k = r < M ? K : 0;
@@ -468,32 +516,28 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
         }
     }
     if (!part) return;
+    // every group's sums side by side over the ring's memory, then a thread adds its columns' in group order
     float* to = part + (int64_t)blockIdx.x * 2 * K;
     [[maybe_unused]] const int64_t parts = (int64_t)(gridDim.x - blockIdx.x) * 2 * K;
-    float* col = reinterpret_cast<float*>(ring);
-    if (groups > 1) {
-        if (VEC) ptx::cp_async_wait<0>();
-        __syncthreads();
-        for (int k = threadIdx.x; k < 2 * K; k += blockDim.x) col[k] = 0.0f;
-    }
-    for (int turn = 0; turn < groups; ++turn) {
-        if (groups > 1) __syncthreads();
-        if (g != turn) continue;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) {
-                const int first = unit_first<VEC>(u, width, t), k = VEC ? first + i : first + i * width;
-                const float vw = i % 2 ? sw[u][i / 2].hi() : sw[u][i / 2].lo(), vb = i % 2 ? sb[u][i / 2].hi() : sb[u][i / 2].lo();
-                if (k >= K) continue;
-                if (groups > 1) { col[k] += vw; col[K + k] += vb; }
-                else if (SS1_SPAN_IN(k, K + 1, parts, kSiteNormPart)) { to[k] = vw; to[K + k] = vb; }
-            }
-    }
-    if (groups == 1) return;
+    float* col = reinterpret_cast<float*>(ring) + (int64_t)g * 2 * K;
+    if (kRing) ptx::cp_async_wait<0>();
     __syncthreads();
-    for (int k = threadIdx.x; k < 2 * K; k += blockDim.x)
-        if (SS1_IN(k, parts, kSiteNormPart)) to[k] = col[k];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            const int first = unit_first<VEC>(u, width, t), k = VEC ? first + i : first + i * width;
+            if (k < K) {
+                col[k] = i % 2 ? sw[u][i / 2].hi() : sw[u][i / 2].lo();
+                col[K + k] = i % 2 ? sb[u][i / 2].hi() : sb[u][i / 2].lo();
+            }
+        }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 2 * K; k += blockDim.x) {
+        float v = 0.0f;
+        for (int o = 0; o < groups; ++o) v += reinterpret_cast<float*>(ring)[(int64_t)o * 2 * K + k];
+        if (SS1_IN(k, parts, kSiteNormPart)) to[k] = v;
+    }
 }
 
 // Rows wider than kBwdWidest: dX a row per CTA in two passes, and the column sums apart.
@@ -563,9 +607,9 @@ cudaError_t bwd_rows(const void* dY, const void* X, const float* mean, const flo
                      int K, int ctas, cudaStream_t st) {
     auto* fn = &norm_bwd_kernel<T, W, VEC, UNITS, ROWS>;
     const int width = bwd_group_threads(K), groups = bwd_groups(K);
-    // the turns ahead, and the groups' sums over them: K <= 8 * kBwdThreads / 2 where there are several groups
-    constexpr int most_sums = 2 * (kBwdThreads / 2) * kUnit * (int)sizeof(float);
-    constexpr int turns = VEC ? bwd_ahead<T>() * 4 * pieces<T>() * kBwdThreads * 16 : 0, smem = turns > most_sums ? turns : most_sums;
+    // the turns ahead, and the groups' sums over them: a group has at most 16 columns a thread
+    constexpr int most_sums = 2 * kBwdThreads * UNITS * kUnit * (int)sizeof(float);
+    constexpr int turns = in_ring<T, VEC>() ? bwd_ahead<T>() * 4 * unit_bytes<T>() * kBwdThreads : 0, smem = turns > most_sums ? turns : most_sums;
     const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
     fn<<<(unsigned)ctas, width * groups, smem, st>>>((const T*)dY, (const T*)X, mean, rstd, (const W*)w, (T*)dX, part, M, K, width, groups);
