@@ -226,7 +226,7 @@ __device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Fa
 }
 
 template <int N, int BITS>
-__global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
+__global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
                                                             const float* __restrict__ device, float minus_zero) {
     const F2 none = F2::both(minus_zero);
     Factors f = host;
