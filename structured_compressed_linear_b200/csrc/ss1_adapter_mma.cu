@@ -29,10 +29,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
 // d += a b: 16 x 8 float32, a 16 x 16 (rows g, g + 8 of lane / 4), b 16 x 8.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -52,6 +48,50 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     const __nv_bfloat162 l = __floats2bfloat162_rn(fabsf(fx) < INFINITY ? x - fx : 0.0f, fabsf(fy) < INFINITY ? y - fy : 0.0f);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Instruction descriptor for operands whose contiguous side is M (A) or N (B): bits 15 and 16.
+__host__ __device__ constexpr uint32_t idesc_mn(int N, bool a_mn, bool b_mn) {
+    return ptx::idesc_bf16_f32(128, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+// A swizzled [rows][64] box in shared memory, 128 bytes a row, as an operand with the rows along the reduction: 8 rows are
+// one 1024-byte atom, `next` bytes lead to the box of the next 64 elements.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t next) { return ptx::smem_desc(at, next, 1024, ptx::kLayoutSW128); }
+// The same kind of box with the rows along M or N.
+__device__ __forceinline__ uint64_t desc_k(uint32_t at) { return ptx::smem_desc(at, 16, 1024, ptx::kLayoutSW128); }
+
+// The tensor core's part of a CTA: one completion barrier a ring slot, and what says that a wait gave up (after two
+// seconds, where the products of a stage take a microsecond). Then nothing is waited for any more and
+// the CTA's results are NaN.
+constexpr int kSlots = 6;
+struct TensorState {
+    uint64_t done[kSlots];
+    uint32_t tmem;
+    int gave_up;
+};
+__device__ __forceinline__ void tensor_begin(TensorState& t, uint32_t columns) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&t.done[i], 1);
+        t.gave_up = 0;
+        ptx::fence_mbar_init();
+    }
+    if (threadIdx.x < 32) {
+        ptx::tmem_alloc(&t.tmem, columns);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+}
+__device__ __forceinline__ void tensor_wait(TensorState& t, int slot, uint32_t parity) {
+    if (!ptx::mbar_wait(&t.done[slot], parity, &t.gave_up, 2000000000ull)) *(volatile int*)&t.gave_up = 1;
+}
+// All threads, after the last wait and the last read of tensor memory.
+__device__ __forceinline__ void tensor_end(TensorState& t, uint32_t columns) {
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (threadIdx.x < 32) ptx::tmem_dealloc(t.tmem, columns);
 }
 
 struct Tile {
@@ -141,20 +181,21 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, Plan
 // One cluster per tile of 128 rows, its CTAs taking equal shares of the columns: the partial
 // products meet in distributed shared memory and are added in CTA order. 256 threads: warp w owns rows
 // 16 w .. 16 w + 15. Stages of 64 columns: U [128][64] in 128-byte rows with the 16-byte chunks
-// XOR-swizzled by the row, and T either [RT][64] likewise (TRANS false: T_a is [R, C]) or [64][RT] in padded
-// rows (TRANS true: T_a is [C, ld]). Each stage's MMAs start from zero and are added in float32:
-// the tensor core's own accumulation truncates, over thousands of columns by more than float32's rounding.
+// XOR-swizzled by the row, and T likewise: [RT][64] (TRANS false: T_a is [R, C]) or boxes of [64][64] (TRANS true: T_a
+// is [C, ld]). H (TRANS false) is handed out in float32, so each stage's MMAs start from zero and are
+// added in registers: the tensor core's own accumulation truncates, over thousands of columns by more than
+// float32's rounding. G (TRANS true) only feeds bf16 results: tcgen05 multiplies out of the ring as it lies
+// there and accumulates in tensor memory, one thread issuing four instructions a stage.
 constexpr int kStages = 4;
 
 template <int RT, bool TRANS>
 struct ProductsShape {
     static constexpr int u_bytes = kTile * 128;
-    static constexpr int t_pitch = TRANS ? RT * 2 + 16 : 128;
-    static constexpr int t_bytes = TRANS ? 64 * t_pitch : RT * 128;
+    static constexpr int t_bytes = TRANS ? (RT + 63) / 64 * 64 * 128 : RT * 128;
     static constexpr int stage = u_bytes + t_bytes;
     static constexpr int pitch = RT + 4;                       // floats of a row of partial products
     static constexpr int ring = kStages * stage, sums = kTile * pitch * 4;
-    static constexpr int smem = (ring > sums ? ring : sums) + 128;
+    static constexpr int smem = (ring > sums ? ring : sums) + 1024;
 };
 
 struct Products {
@@ -168,8 +209,8 @@ struct Products {
 };
 
 template <int RT, bool TRANS>
-__device__ __forceinline__ void products_role(const Products& d, const PlanView& plan, int tile_index, uint8_t* raw, int M, int R,
-                                              int n) {
+__device__ __forceinline__ void products_role(const Products& d, const PlanView& plan, int tile_index, uint8_t* raw, TensorState& ts, int M,
+                                              int R, int n) {
     using S = ProductsShape<RT, TRANS>;
     const bf16 *U = d.U, *table = d.table;
     const float* scale = d.scale;
@@ -195,7 +236,7 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
             }
         return;
     }
-    const uint32_t base = (ptx::smem_u32(raw) + 127u) & ~127u;
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     const bf16* T = table + (int64_t)tile.adapter * C * (TRANS ? ld : R);
     const int chunks = (C + 63) / 64, per = (chunks + splits - 1) / splits;
     const int from = min(chunks, split * per), to = min(chunks, from + per);
@@ -224,7 +265,7 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
         tok[i] = k < kPieces && r < (TRANS ? ld : R);
         tcol[i] = from * 64 + c;
         tp[i] = T + (tok[i] ? (TRANS ? (int64_t)tcol[i] * ld + r : (int64_t)r * C + tcol[i]) : 0);
-        tdst[i] = S::u_bytes + (TRANS ? c * S::t_pitch + r * 2 : r * 128 + (((k % 8) ^ (r & 7)) << 4));
+        tdst[i] = S::u_bytes + (TRANS ? r / 64 * 8192 + c * 128 + (((r / 8 % 8) ^ (c & 7)) << 4) : r * 128 + (((k % 8) ^ (r & 7)) << 4));
     }
     int ucol = from * 64 + uc * 8;
     auto load = [&](bool some, int slot) {      // the next stage in line
@@ -249,64 +290,102 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
         ptx::cp_async_commit();
     };
 
-    float sum[RT / 8][4];
-#pragma unroll
-    for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[j][i] = 0.0f;
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) load(from + s < to, s);
-    const bool busy = warp * 16 < tile.rows;
-    for (int first = from; first < to; first += kStages)
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            const int chunk = first + s;
-            if (chunk >= to) break;
+    float* part = reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw)));   // later, over the ring's memory
+    if (TRANS) {
+        constexpr uint32_t kColumns = RT < 32 ? 32 : RT, kInstr = idesc_mn(RT, false, true);
+        tensor_begin(ts, kColumns);
+        const uint32_t tmem = ts.tmem;
+        for (int chunk = from, slot = 0; chunk < to; ++chunk, slot = slot + 1 == kStages ? 0 : slot + 1) {
             ptx::cp_async_wait<kStages - 2>();
+            ptx::fence_proxy_async_smem();
             __syncthreads();
-            load(chunk + kStages - 1 < to, (s + kStages - 1) % kStages);
-            if (!busy) continue;
-            const uint32_t su = base + s * S::stage, stt = su + S::u_bytes;
-            float acc[RT / 8][4];
+            if (tid == 0) {
+                const uint32_t su = base + slot * S::stage, stt = su + S::u_bytes;
 #pragma unroll
-            for (int j = 0; j < RT / 8; ++j)
+                for (int k = 0; k < 4; ++k)
+                    ptx::umma_bf16_ss(tmem, desc_k(su + k * 32), desc_mn(stt + k * 2048, 8192), kInstr, chunk > from || k > 0);
+                ptx::umma_commit(&ts.done[slot]);
+            }
+            const int last = slot == 0 ? kStages - 1 : slot - 1;      // the slot of the stage before: loaded again once read
+            if (chunk > from) tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1);
+            load(chunk + kStages - 1 < to, last);
+        }
+        if (to > from) tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1);
+        ptx::cp_async_wait<0>();
+        ptx::tc_fence_after();
+        __syncthreads();
+        const bool valid = *(volatile int*)&ts.gave_up == 0;
+        if (warp < 4) {                                               // lane = row of the tile
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+            for (int j = 0; j < RT; j += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(warp * 32) << 16) + j, v);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_fence_regs<16>(v);
+                float4* to_row = reinterpret_cast<float4*>(part + tid * S::pitch + j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t a[4];
-                const int ar = warp * 16 + lane % 16;
-                ldsm4(a, su + ar * 128 + (((k * 2 + lane / 16) ^ (ar & 7)) << 4));
+                for (int i = 0; i < 4; ++i) {
+                    float x[4];
 #pragma unroll
-                for (int j = 0; j < RT / 8; j += 2) {
-                    uint32_t b[4];
-                    const int mat = lane / 8, l8 = lane % 8;
-                    if (TRANS) {
-                        ldsm4_trans(b, stt + (k * 16 + (mat % 2) * 8 + l8) * S::t_pitch + (j + mat / 2) * 16);
-                    } else {
-                        const int r = (j + mat / 2) * 8 + l8;
-                        ldsm4(b, stt + r * 128 + (((k * 2 + mat % 2) ^ (r & 7)) << 4));
-                    }
-                    mma16816(acc[j], a, b[0], b[1]);
-                    mma16816(acc[j + 1], a, b[2], b[3]);
+                    for (int k = 0; k < 4; ++k) x[k] = to > from ? (valid ? __uint_as_float(v[4 * i + k]) : NAN) : 0.0f;
+                    to_row[i] = make_float4(x[0], x[1], x[2], x[3]);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[j][i] += acc[j][i];
         }
-    ptx::cp_async_wait<0>();
-    wait_for_previous();
-    __syncthreads();
-    // the partial products over the ring's memory
-    float* part = reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw)));
+        tensor_end(ts, kColumns);
+    } else {
+        float sum[RT / 8][4];
 #pragma unroll
-    for (int j = 0; j < RT / 8; ++j) {
-        const int r = warp * 16 + lane / 4, c = j * 8 + (lane % 4) * 2;
-        *reinterpret_cast<float2*>(part + r * S::pitch + c) = make_float2(sum[j][0], sum[j][1]);
-        *reinterpret_cast<float2*>(part + (r + 8) * S::pitch + c) = make_float2(sum[j][2], sum[j][3]);
+        for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[j][i] = 0.0f;
+        const bool busy = warp * 16 < tile.rows;
+        for (int first = from; first < to; first += kStages)
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                const int chunk = first + s;
+                if (chunk >= to) break;
+                ptx::cp_async_wait<kStages - 2>();
+                __syncthreads();
+                load(chunk + kStages - 1 < to, (s + kStages - 1) % kStages);
+                if (!busy) continue;
+                const uint32_t su = base + s * S::stage, stt = su + S::u_bytes;
+                float acc[RT / 8][4];
+#pragma unroll
+                for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4];
+                    const int ar = warp * 16 + lane % 16;
+                    ldsm4(a, su + ar * 128 + (((k * 2 + lane / 16) ^ (ar & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < RT / 8; j += 2) {
+                        uint32_t b[4];
+                        const int mat = lane / 8, l8 = lane % 8, r = (j + mat / 2) * 8 + l8;
+                        ldsm4(b, stt + r * 128 + (((k * 2 + mat % 2) ^ (r & 7)) << 4));
+                        mma16816(acc[j], a, b[0], b[1]);
+                        mma16816(acc[j + 1], a, b[2], b[3]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[j][i] += acc[j][i];
+            }
+        ptx::cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < RT / 8; ++j) {
+            const int r = warp * 16 + lane / 4, c = j * 8 + (lane % 4) * 2;
+            *reinterpret_cast<float2*>(part + r * S::pitch + c) = make_float2(sum[j][0], sum[j][1]);
+            *reinterpret_cast<float2*>(part + (r + 8) * S::pitch + c) = make_float2(sum[j][2], sum[j][3]);
+        }
     }
+    wait_for_previous();
     if (splits > 1) ptx::cluster_sync();
     else __syncthreads();
     const float f = scale ? scale[tile.adapter] : 1.0f;
@@ -344,8 +423,9 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
 template <int RT>
 __global__ void __launch_bounds__(kThreads) products_kernel(const Products d, PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
+    __shared__ TensorState unused;
     let_next_start();
-    products_role<RT, false>(d, plan, blockIdx.y, raw, M, R, n);
+    products_role<RT, false>(d, plan, blockIdx.y, raw, unused, M, R, n);
 }
 
 // ---- update ----------------------------------------------------------------------------------
@@ -552,20 +632,24 @@ __global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, Pla
 // ---- columns ---------------------------------------------------------------------------------
 
 // A CTA takes 256 columns and a run of tiles, 32 rows a stage: U as four [32][64] boxes in swizzled
-// 128-byte rows, P's packed rows in padded ones. Warp w owns columns 32 w .. 32 w + 31: U transposed
-// out of shared memory is the A operand (column x row), P the B operand, and the sums stay in registers
-// until the run comes to another adapter. The tiles are dealt evenly whatever their adapters: run k's sums
-// for adapter a go to part[k + a] (k and a only grow along the list, so no two share a place), or
-// straight to `out` where the run has all of the adapter's tiles.
+// 128-byte rows, P's packed rows as boxes of the same kind. The reduction runs over the rows, so both
+// operands of D[column, rank] are read along their rows' contiguous side, as they lie: tcgen05 takes 2 x 128
+// columns x (first parts, second parts) a stage from one thread, and D stays in tensor memory until the
+// run comes to another adapter, when the two parts' sums are added. (With mma.sync, whose fragments cost
+// every warp transposed loads and registers, a stage took 1.2 us at rank 32: 29 us for G and dB at
+// 8192 x 2304.) The tiles are dealt evenly whatever their adapters: run k's sums for adapter a go to part[k + a]
+// (k and a only grow along the list, so no two share a place), or straight to `out` where the run has
+// all of the adapter's tiles.
 constexpr int kColCols = 256, kColRows = 32, kColSteps = kTile / kColRows;
 
 template <int RT>
 struct ColumnsShape {
-    static constexpr int u_bytes = kColRows * kColCols * 2;
-    static constexpr int p_pitch = RT * 4 + 16;
-    static constexpr int stage = u_bytes + kColRows * p_pitch;
+    static constexpr int box = kColRows * 128;
+    static constexpr int u_bytes = kColCols / 64 * box, p_boxes = (2 * RT + 63) / 64;
+    static constexpr int stage = u_bytes + p_boxes * box;
     static constexpr int stages = RT <= 32 ? 5 : (RT <= 64 ? 4 : 3);
-    static constexpr int smem = stages * stage + 128;
+    static constexpr int smem = stages * stage + 1024;
+    static constexpr uint32_t columns = 2 * 2 * RT;            // of tensor memory
 };
 
 struct Columns {
@@ -588,10 +672,11 @@ __device__ __forceinline__ int tiles_a_run(const PlanView& plan, int n, int M, i
 }
 
 template <int RT>
-__device__ __forceinline__ void columns_role(const Columns& d, const PlanView& plan, int range, int run, uint8_t* raw, int M, int R,
-                                             int n) {
+__device__ __forceinline__ void columns_role(const Columns& d, const PlanView& plan, int range, int run, uint8_t* raw, TensorState& ts,
+                                             int M, int R, int n) {
     using S = ColumnsShape<RT>;
-    const uint32_t base = (ptx::smem_u32(raw) + 127u) & ~127u;
+    static_assert(S::stages <= kSlots, "a barrier a slot");
+    const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int C = d.C, c0 = range * kColCols;
     const int tiles = adapter_tiles(plan, n - 1, M).y, per = tiles_a_run(plan, n, M, d.runs);
@@ -633,7 +718,8 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
                 const int e = tid + i * kThreads, r = e / (RT / 4), c = (e % (RT / 4)) * 8;
                 const int64_t at = (int64_t)(now.first + k * kColRows + r) * 2 * RT + c;
                 const bool ok = k * kColRows + r < now.rows && SS1_SPAN_IN(at, 8, (int64_t)M * 2 * RT, kSiteAdaG);
-                if (kPieces % kThreads == 0 || e < kPieces) copy16(sp + r * S::p_pitch + c * 2, ok ? d.packed + at : d.packed, ok);
+                if (kPieces % kThreads == 0 || e < kPieces)
+                    copy16(sp + c / 64 * S::box + r * 128 + (((c / 8 % 8) ^ (r & 7)) << 4), ok ? d.packed + at : d.packed, ok);
             }
             if (k == kColSteps - 1) {
                 now = next;
@@ -646,76 +732,71 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
         ptx::cp_async_commit();
     };
 
-    float acc[2][RT / 8][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[h][j][i] = 0.0f;
     int adapter = now.adapter, next_adapter = adapter;
     for (int s = 0; s < S::stages - 1; ++s) load(s, s);
-    const bool busy = c0 + warp * 32 < C;
+    tensor_begin(ts, S::columns);
+    const uint32_t tmem = ts.tmem;
+    constexpr uint32_t kInstr = idesc_mn(2 * RT, true, true);
     const int64_t size = (int64_t)C * R;
+    bool fresh = true;
     for (int step = 0, slot = 0;; ++step) {
         if (step % kColSteps == 0 || step == steps) {       // a tile begins, or the run ends
             const int a = step < steps ? next_adapter : -1;
             if (step + kColSteps < steps) next_adapter = tile_of(plan, t0 + step / kColSteps + 1, M).adapter;
-            if (a != adapter && busy && (unsigned)adapter < (unsigned)n) {
+            if (a != adapter && (unsigned)adapter < (unsigned)n) {
+                tensor_wait(ts, slot == 0 ? S::stages - 1 : slot - 1, ((step - 1) / S::stages) & 1);
+                ptx::tc_fence_after();
+                const bool valid = *(volatile int*)&ts.gave_up == 0;
                 const int2 own = adapter_tiles(plan, adapter, M);
                 const bool whole = own.x >= t0 && own.y <= t1;
                 const int64_t place = whole ? adapter * size : (int64_t)(run + adapter) * size;
                 [[maybe_unused]] const int64_t all = (whole ? n : d.runs + n) * size;
+                const int c = c0 + warp * 32 + lane;        // warps 0 - 3: the first 128 columns, lane by lane; 4 - 7 the others
+                const uint32_t from_lane = tmem + warp / 4 * 2 * RT + ((uint32_t)(warp % 4 * 32) << 16);
+                for (int j = 0; j < RT && j < R; j += 16) {
+                    uint32_t hi[16], lo[16];
+                    ptx::tmem_ld_32x32b_x16(from_lane + j, hi);
+                    ptx::tmem_ld_32x32b_x16(from_lane + RT + j, lo);
+                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_fence_regs<16>(hi);
+                    ptx::tmem_ld_fence_regs<16>(lo);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < RT / 8; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = c0 + warp * 32 + h * 16 + lane / 4 + (i / 2) * 8, r = j * 8 + (lane % 4) * 2 + i % 2;
-                            const int64_t at = place + (int64_t)c * d.cs + (int64_t)r * d.rs;
-                            if (c < C && r < R && SS1_IN(at, all, kSiteAdaPart)) {
-                                if (whole) d.out[at] = __float2bfloat16_rn(acc[h][j][i]);
-                                else d.part[at] = acc[h][j][i];
-                            }
-                            acc[h][j][i] = 0.0f;
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = valid ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : NAN;
+                        const int64_t at = place + (int64_t)c * d.cs + (int64_t)(j + i) * d.rs;
+                        if (c >= C || j + i >= R || !SS1_IN(at, all, kSiteAdaPart)) continue;
+                        if (whole) d.out[at] = __float2bfloat16_rn(v);
+                        else d.part[at] = v;
+                    }
+                }
+                ptx::tc_fence_before();
+                fresh = true;      // the barrier below comes before the next product overwrites what was read
             }
             adapter = a;
             if (step == steps) break;
         }
         ptx::cp_async_wait<S::stages - 2>();
+        ptx::fence_proxy_async_smem();
         __syncthreads();
-        load(step + S::stages - 1, slot == 0 ? S::stages - 1 : slot - 1);
-        const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
-        slot = slot == S::stages - 1 ? 0 : slot + 1;
-        if (!busy) continue;
-        const int mat = lane / 8, l8 = lane % 8;
+        if (tid == 0) {
+            const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
+            ptx::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kColRows / 16; ++k) {
-            uint32_t u[2][4];
+            for (int k = 0; k < kColRows / 16; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = k * 16 + (mat / 2) * 8 + l8, chunk = warp * 4 + h * 2 + mat % 2;
-                ldsm4_trans(u[h], su + (chunk / 8) * (kColRows * 128) + r * 128 + (((chunk % 8) ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int j = 0; j < RT / 8; j += 2) {
-                uint32_t b[4], l[4];
-                const uint32_t at = sp + (k * 16 + (mat % 2) * 8 + l8) * S::p_pitch + (j + mat / 2) * 16;
-                ldsm4_trans(b, at);
-                ldsm4_trans(l, at + RT * 2);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mma16816(acc[h][j], u[h], l[0], l[1]);
-                    mma16816(acc[h][j + 1], u[h], l[2], l[3]);
-                    mma16816(acc[h][j], u[h], b[0], b[1]);
-                    mma16816(acc[h][j + 1], u[h], b[2], b[3]);
-                }
-            }
+                for (int h = 0; h < 2; ++h)
+                    ptx::umma_bf16_ss(tmem + h * 2 * RT, desc_mn(su + h * 2 * S::box + k * 2048, S::box), desc_mn(sp + k * 2048, S::box), kInstr,
+                                      !fresh || k > 0);
+            ptx::umma_commit(&ts.done[slot]);
         }
+        fresh = false;
+        const int last = slot == 0 ? S::stages - 1 : slot - 1;        // the slot of the step before: loaded again once read
+        if (step > 0) tensor_wait(ts, last, ((step - 1) / S::stages) & 1);
+        load(step + S::stages - 1, last);
+        slot = slot == S::stages - 1 ? 0 : slot + 1;
     }
     ptx::cp_async_wait<0>();
+    tensor_end(ts, S::columns);
 }
 
 // G and dB in one launch: both read dY (from HBM once: the other reader finds it in L2). The first `tiles` rows of
@@ -729,13 +810,14 @@ template <int RT>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) first_gradients_kernel(const Products g, int tiles, const Columns db, int nb,
                                                                                      PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
+    __shared__ TensorState ts;
     let_next_start();
     if ((int)blockIdx.y < tiles) {
-        products_role<RT, true>(g, plan, blockIdx.y, raw, M, R, n);
+        products_role<RT, true>(g, plan, blockIdx.y, raw, ts, M, R, n);
     } else {
         wait_for_previous();      // the packed H
         const int k = ((int)blockIdx.y - tiles) * gridDim.x + blockIdx.x, ranges = (db.C + kColCols - 1) / kColCols;
-        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, M, R, n);
+        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, ts, M, R, n);
     }
 }
 
@@ -749,12 +831,13 @@ template <int RT>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_kernel(const Columns da, int na, const Update dx,
                                                                                       PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
+    __shared__ TensorState ts;
     let_next_start();
     wait_for_previous();
     const int i = blockIdx.x;
     if (i < na) {
         const int ranges = (da.C + kColCols - 1) / kColCols;
-        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, M, R, n);
+        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, ts, M, R, n);
     } else {
         update_role<RT>(dx, plan, tile_of(plan, (i - na) / dx.splits, M), (i - na) % dx.splits, raw, M, R, n, true);
     }
