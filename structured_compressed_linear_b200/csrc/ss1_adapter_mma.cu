@@ -159,19 +159,25 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, Plan
         return;
     }
     cta -= d.nb;
-    const int kb = (d.K + 31) / 32, rb = (d.ld + 31) / 32;
-    for (int64_t i = cta; i < (int64_t)kb * rb * n; i += d.na) {
-        const int k0 = (int)(i % kb) * 32, r0 = (int)(i / kb % rb) * 32, a = (int)(i / kb / rb);
+    const int kb = (d.K + 31) / 32, rb = (d.ld + 31) / 32;      // below 2^30 boxes in all
+    for (int i = cta; i < kb * rb * n; i += d.na) {
+        const int k0 = i % kb * 32, r0 = i / kb % rb * 32, a = i / kb / rb;
+        const bf16* from = d.A + (int64_t)a * R * d.K;
+        bf16* to = d.turned_a + (int64_t)a * d.K * d.ld;
         __syncthreads();
-        for (int y = tid / 32; y < 32; y += kThreads / 32) {
-            const int k = k0 + tid % 32, r = r0 + y;
-            const int64_t at = ((int64_t)a * R + r) * d.K + k;
-            box[y][tid % 32] = r < R && k < d.K && SS1_IN(at, (int64_t)n * R * d.K, kSiteAdaA) ? d.A[at] : __float2bfloat16_rn(0.0f);
+        const int k = k0 + tid % 32;
+#pragma unroll
+        for (int y = 0; y < 32; y += kThreads / 32) {
+            const int r = r0 + y + tid / 32;
+            box[y + tid / 32][tid % 32] = r < R && k < d.K && SS1_IN(((int64_t)a * R + r) * d.K + k, (int64_t)n * R * d.K, kSiteAdaA)
+                                              ? from[(int64_t)r * d.K + k] : __float2bfloat16_rn(0.0f);
         }
         __syncthreads();
-        for (int y = tid / 32; y < 32; y += kThreads / 32) {
-            const int k = k0 + y, r = r0 + tid % 32;
-            if (k < d.K && r < d.ld) d.turned_a[((int64_t)a * d.K + k) * d.ld + r] = box[tid % 32][y];
+        const int r = r0 + tid % 32;
+#pragma unroll
+        for (int y = 0; y < 32; y += kThreads / 32) {
+            const int kk = k0 + y + tid / 32;
+            if (kk < d.K && r < d.ld) to[(int64_t)kk * d.ld + r] = box[tid % 32][y + tid / 32];
         }
     }
 }
@@ -844,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_k
 }
 
 // The runs' partial sums, in run order, for the adapters whose tiles lie in several runs; zeros for those
-// without rows. y = 0: dA, 1: dB; z: adapters.
+// without rows. y = 0: dA, 1: dB.
 struct Sums {
     const float* part[2];
     bf16* out[2];
@@ -852,21 +858,46 @@ struct Sums {
     int runs[2];
 };
 __global__ void __launch_bounds__(kThreads) add_kernel(const Sums s, PlanView plan, int M, int n) {
+    __shared__ int16_t runs_of[kMaxCount][2];
     wait_for_previous();
     const int w = blockIdx.y;
     if (s.out[w] == nullptr) return;
     const int64_t size = s.size[w];
     const int per = tiles_a_run(plan, n, M, s.runs[w]);
-    for (int a = blockIdx.z; a < n; a += gridDim.z) {
+    // every adapter's first and last run, all looked up at once
+    for (int a = threadIdx.x; a < n; a += kThreads) {
         const int2 own = adapter_tiles(plan, a, M);
         const int lo = own.x / per, hi = own.y > own.x ? min((own.y - 1) / per, s.runs[w] - 1) : lo - 1;
-        if (lo == hi) continue;          // written by the run itself
-        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += (int64_t)gridDim.x * kThreads) {
-            float v = 0.0f;
-            for (int k = lo; k <= hi; ++k) v += s.part[w][(int64_t)(k + a) * size + i];
-            s.out[w][a * size + i] = __float2bfloat16_rn(v);
-        }
+        runs_of[a][0] = (int16_t)lo;
+        runs_of[a][1] = (int16_t)hi;
     }
+    __syncthreads();
+    const bool vec = size % 4 == 0;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * kThreads * 4)
+        for (int a = 0; a < n; ++a) {
+            const int lo = runs_of[a][0], hi = runs_of[a][1];
+            if (lo == hi) continue;          // written by the run itself
+            const float* p = s.part[w] + (int64_t)(lo + a) * size + i;
+            bf16* to = s.out[w] + a * size + i;
+            if (vec) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int k = lo; k <= hi; ++k, p += size) {
+                    const float4 u = *reinterpret_cast<const float4*>(p);
+                    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                }
+                to[0] = __float2bfloat16_rn(v.x);
+                to[1] = __float2bfloat16_rn(v.y);
+                to[2] = __float2bfloat16_rn(v.z);
+                to[3] = __float2bfloat16_rn(v.w);
+            } else {
+                for (int e = 0; e < 4 && i + e < size; ++e) {
+                    float v = 0.0f;
+                    for (int k = lo; k <= hi; ++k) v += p[(int64_t)(k - lo) * size + e];
+                    to[e] = __float2bfloat16_rn(v);
+                }
+            }
+        }
 }
 
 // ---- launches --------------------------------------------------------------------------------
@@ -993,9 +1024,8 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
     Sums s = {};
     if (dA) { s.part[0] = da.part; s.out[0] = da.out; s.size[0] = (int64_t)c.K * c.R; s.runs[0] = ra; }
     if (dB) { s.part[1] = db.part; s.out[1] = db.out; s.size[1] = (int64_t)c.N * c.R; s.runs[1] = rb; }
-    const int64_t size = s.size[0] > s.size[1] ? s.size[0] : s.size[1], blocks = (size + kThreads - 1) / kThreads;
-    return launch_dependent(&add_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), 2, (unsigned)(c.n < 64 ? c.n : 64)),
-                            dim3(kThreads), 0, st, s, c.plan, (int)c.M, c.n);
+    const int64_t size = s.size[0] > s.size[1] ? s.size[0] : s.size[1], blocks = (size + 4 * kThreads - 1) / (4 * kThreads);
+    return launch_dependent(&add_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), 2), dim3(kThreads), 0, st, s, c.plan, (int)c.M, c.n);
 }
 
 }  // namespace
