@@ -29,9 +29,9 @@ using namespace op;
 // One CTA. Every warp counts its own contiguous share of the rows by adapter (lanes with the same
 // adapter find one another by a ballot for each bit of its number: one __match_any_sync takes a step for every
 // different value, 18 us for 8192 rows of 32 adapters in random order), the counts are scanned over
-// adapters and warps, and the same walk again gives each row its place: rows keep their order within an
-// adapter. The first kAhead index words of a lane are loaded together and kept for the second walk (32
-// warps cover 16,384 rows that way): one memory latency instead of one for every 32 rows, twice.
+// adapters and warps, and each row's place is what comes before it: rows keep their order within an
+// adapter. The first kAhead index words of a lane are loaded together, and their places within the warp kept
+// (32 warps cover 16,384 rows that way): one memory latency, and one walk; rows beyond are walked twice.
 constexpr int kAhead = 16;
 
 __device__ __forceinline__ int plan_group(const int32_t* __restrict__ index, int row, int end, int n) {
@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     int* mine = cnt + warp * groups;
     const int bits = 32 - __clz(n);           // of the numbers 0 .. n
     auto peers = [&](int a) {                  // lanes with this lane's group; -1 (no row) is a group of its own
+        const int one = __shfl_sync(0xFFFFFFFFu, a, 0);
+        if (__all_sync(0xFFFFFFFFu, a == one)) return 0xFFFFFFFFu;      // a request's rows mostly come together
         unsigned same = __ballot_sync(0xFFFFFFFFu, a >= 0);
         if (a < 0) same = ~same;
         for (int b = 0; b < bits; ++b) {
@@ -64,14 +66,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
         }
         return same;
     };
+    // the row's number among the warp's rows of its group so far
     auto count = [&](int a) {
         const unsigned same = peers(a);
+        const int before = a >= 0 ? mine[a] + __popc(same & ((1u << lane) - 1u)) : 0;
+        __syncwarp();
         if (a >= 0 && lane == __ffs(same) - 1) mine[a] += __popc(same);
         __syncwarp();
+        return before;
     };
+    int nth[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (begin + i * 32 < end) count(ahead[i]);
+    for (int i = 0; i < kAhead; ++i) nth[i] = begin + i * 32 < end ? count(ahead[i]) : 0;
     for (int at = begin + kAhead * 32; at < end; at += 32) count(plan_group(index, at + lane, end, n));
     __syncthreads();
     // totals, then their exclusive sums (one warp, 32 groups at a time), with the tiles' beside them
@@ -130,21 +136,24 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
         }
         plan.tiles[i] = t;
     }
-    auto place = [&](int a, int row) {
-        const unsigned same = peers(a);
-        int to = 0;
-        if (a >= 0) to = first[a] + mine[a] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (a >= 0) {
-            if (lane == __ffs(same) - 1) mine[a] += __popc(same);
-            if (SS1_IN(to, M, kSitePlan)) plan.rows[to] = row;
-        }
-        __syncwarp();
+    int* so_far = cnt + warp * groups;         // rows of the group in the warps before this one; then its own ones too
+    auto put = [&](int a, int row, int number) {
+        const int to = first[a] + number;
+        if (SS1_IN(to, M, kSitePlan)) plan.rows[to] = row;
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (begin + i * 32 < end) place(ahead[i], begin + i * 32 + lane);
-    for (int at = begin + kAhead * 32; at < end; at += 32) place(plan_group(index, at + lane, end, n), at + lane);
+        if (ahead[i] >= 0) put(ahead[i], begin + i * 32 + lane, so_far[ahead[i]] + nth[i]);
+    if (begin + kAhead * 32 >= end) return;    // the whole warp
+    __syncwarp();
+    // the second walk counts on from the first kAhead rounds
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) count(ahead[i]);
+    for (int at = begin + kAhead * 32; at < end; at += 32) {
+        const int a = plan_group(index, at + lane, end, n);
+        const int number = count(a);
+        if (a >= 0) put(a, at + lane, number);
+    }
 }
 
 cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, cudaStream_t st) {

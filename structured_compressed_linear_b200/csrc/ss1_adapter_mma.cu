@@ -664,6 +664,7 @@ struct Columns {
     bf16* out;
     float* part;
     int C, cs, rs, runs;
+    bool vec;           // ranks consecutive (rs 1), R a multiple of 8, `out` on a 16-byte boundary
 };
 
 // Adapter a's tiles, and the tiles of a run.
@@ -766,13 +767,33 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
                     ptx::tmem_ld_wait();
                     ptx::tmem_ld_fence_regs<16>(hi);
                     ptx::tmem_ld_fence_regs<16>(lo);
+                    float v[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float v = valid ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : NAN;
-                        const int64_t at = place + (int64_t)c * d.cs + (int64_t)(j + i) * d.rs;
-                        if (c >= C || j + i >= R || !SS1_IN(at, all, kSiteAdaPart)) continue;
-                        if (whole) d.out[at] = __float2bfloat16_rn(v);
-                        else d.part[at] = v;
+                    for (int i = 0; i < 16; ++i) v[i] = valid ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : NAN;
+                    if (c >= C) continue;
+                    const int64_t first = place + (int64_t)c * d.cs + (int64_t)j * d.rs;
+                    if (d.vec) {       // a lane's ranks lie together: element by element each would be a sector of its own
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) {
+                            if (j + i >= R || !SS1_SPAN_IN(first + i, 8, all, kSiteAdaPart)) continue;
+                            if (whole) {
+                                Raw8<bf16> r;
+                                const float w[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
+                                r.set(w);
+                                r.store(d.out + first + i);
+                            } else {
+                                *reinterpret_cast<float4*>(d.part + first + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                *reinterpret_cast<float4*>(d.part + first + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int64_t at = first + (int64_t)i * d.rs;
+                            if (j + i >= R || !SS1_IN(at, all, kSiteAdaPart)) continue;
+                            if (whole) d.out[at] = __float2bfloat16_rn(v[i]);
+                            else d.part[at] = v[i];
+                        }
                     }
                 }
                 ptx::tc_fence_before();
@@ -850,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_k
 }
 
 // The runs' partial sums, in run order, for the adapters whose tiles lie in several runs; zeros for those
-// without rows. y = 0: dA, 1: dB.
+// without rows. y = 0: dA, 1: dB; z: adapters in turn.
 struct Sums {
     const float* part[2];
     bf16* out[2];
@@ -874,7 +895,7 @@ __global__ void __launch_bounds__(kThreads) add_kernel(const Sums s, PlanView pl
     __syncthreads();
     const bool vec = size % 4 == 0;
     for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * kThreads * 4)
-        for (int a = 0; a < n; ++a) {
+        for (int a = blockIdx.z; a < n; a += gridDim.z) {
             const int lo = runs_of[a][0], hi = runs_of[a][1];
             if (lo == hi) continue;          // written by the run itself
             const float* p = s.part[w] + (int64_t)(lo + a) * size + i;
@@ -1003,8 +1024,8 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
     if (e == cudaSuccess) e = prepare<RT>(c, w, dB ? H : nullptr, dX != nullptr, dX || dA, &B, &ld, &prepared, st);
     if (e != cudaSuccess) return e;
     const int rb = mma_runs(c.M, c.N, c.n), ra = mma_runs(c.M, c.K, c.n);
-    const Columns db{(const bf16*)dY, (const bf16*)w.packed_h, (bf16*)dB, w.part_b, (int)c.N, c.R, 1, rb};
-    const Columns da{(const bf16*)X, (const bf16*)w.packed_g, (bf16*)dA, w.part_a, (int)c.K, 1, (int)c.K, ra};
+    const Columns db{(const bf16*)dY, (const bf16*)w.packed_h, (bf16*)dB, w.part_b, (int)c.N, c.R, 1, rb, c.R % 8 == 0 && aligned(dB, 16)};
+    const Columns da{(const bf16*)X, (const bf16*)w.packed_g, (bf16*)dA, w.part_a, (int)c.K, 1, (int)c.K, ra, false};
     const int nb = dB ? (db.C + kColCols - 1) / kColCols * rb : 0;
     const int na = dA ? (da.C + kColCols - 1) / kColCols * ra : 0;
     const int tiles = tiles_at_most(c), gtiles = dX || dA ? tiles : 0;
@@ -1025,7 +1046,8 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
     if (dA) { s.part[0] = da.part; s.out[0] = da.out; s.size[0] = (int64_t)c.K * c.R; s.runs[0] = ra; }
     if (dB) { s.part[1] = db.part; s.out[1] = db.out; s.size[1] = (int64_t)c.N * c.R; s.runs[1] = rb; }
     const int64_t size = s.size[0] > s.size[1] ? s.size[0] : s.size[1], blocks = (size + 4 * kThreads - 1) / (4 * kThreads);
-    return launch_dependent(&add_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), 2), dim3(kThreads), 0, st, s, c.plan, (int)c.M, c.n);
+    return launch_dependent(&add_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), 2, (unsigned)(c.n < 4 ? c.n : 4)),
+                            dim3(kThreads), 0, st, s, c.plan, (int)c.M, c.n);
 }
 
 }  // namespace
