@@ -228,6 +228,8 @@ __device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Fa
 template <int N, int BITS>
 __global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
                                                             const float* __restrict__ device, float minus_zero) {
+    wait_for_previous();
+    let_next_start();
     const F2 none = F2::both(minus_zero);
     Factors f = host;
     if (device) {
@@ -280,9 +282,21 @@ cudaError_t launch(const ss1_adamw_tensor* tensors, int64_t count, int bits, con
         chunks += (t.numel + kChunk - 1) / kChunk;
     }
     if (table.count == 0) return cudaSuccess;
-    if (bits == 32) adamw_kernel<N, 32><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device, -0.0f);
-    else adamw_kernel<N, 8><<<(unsigned)chunks, kWarps * 32, 0, st>>>(table, f, device, -0.0f);
-    return cudaGetLastError();
+    // dependent like launch_dependent's, with the table's address instead of copies of it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)chunks);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    Factors factors = f;
+    float minus_zero = -0.0f;
+    void* args[] = {&table, &factors, &device, &minus_zero};
+    return cudaLaunchKernelExC(&cfg, bits == 32 ? reinterpret_cast<const void*>(&adamw_kernel<N, 32>)
+                                                : reinterpret_cast<const void*>(&adamw_kernel<N, 8>), args);
 }
 
 constexpr int kSmall = 32, kLarge = 440;   // tensors of one launch: the parameters are copied at every launch

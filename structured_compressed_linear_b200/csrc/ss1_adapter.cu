@@ -42,6 +42,8 @@ __device__ __forceinline__ int plan_group(const int32_t* __restrict__ index, int
 
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ index, int M, int n, PlanView plan) {
     extern __shared__ int cnt[];   // [warps][n + 1], then [n + 2] first rows and [n + 2] first tiles
+    wait_for_previous();
+    let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int groups = n + 1;      // group n: rows without an adapter
     int* first = cnt + warps * groups;
@@ -161,8 +163,7 @@ cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, c
     int warps = (48 * 1024 / 4 - 2 * (n + 2)) / (n + 1);
     warps = warps > 32 ? 32 : warps;
     const size_t smem = ((size_t)warps * (n + 1) + 2 * (n + 2)) * sizeof(int);
-    plan_kernel<<<1, warps * 32, smem, st>>>(index, (int)M, n, plan);
-    return cudaGetLastError();
+    return launch_dependent(&plan_kernel, dim3(1), dim3((unsigned)(warps * 32)), smem, st, index, (int)M, n, plan);
 }
 
 namespace {

@@ -129,6 +129,7 @@ struct Prepare {
 template <int RT>
 __global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, PlanView plan, int M, int R, int n) {
     __shared__ bf16 box[32][33];
+    wait_for_previous();
     let_next_start();
     const int tid = threadIdx.x;
     int cta = blockIdx.x;
@@ -430,7 +431,8 @@ template <int RT>
 __global__ void __launch_bounds__(kThreads) products_kernel(const Products d, PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
     __shared__ TensorState unused;
-    let_next_start();
+    wait_for_previous();
+    let_next_start();      // update_kernel reads Y and B before its own wait: they are complete here
     products_role<RT, false>(d, plan, blockIdx.y, raw, unused, M, R, n);
 }
 
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) first_gradients_ke
                                                                                      PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
     __shared__ TensorState ts;
-    let_next_start();
+    let_next_start();             // its successors wait first thing
     if ((int)blockIdx.y < tiles) {
         products_role<RT, true>(g, plan, blockIdx.y, raw, ts, M, R, n);
     } else {
@@ -962,8 +964,7 @@ cudaError_t prepare(const Call& c, const MmaSpace& w, const float* H, bool turn_
     }
     *launched = d.nh + d.nb + d.na > 0;
     if (!*launched) return cudaSuccess;
-    prepare_kernel<RT><<<(unsigned)(d.nh + d.nb + d.na), kThreads, 0, st>>>(d, c.plan, (int)c.M, c.R, c.n);
-    return cudaGetLastError();
+    return launch_dependent(&prepare_kernel<RT>, dim3((unsigned)(d.nh + d.nb + d.na)), dim3(kThreads), 0, st, d, c.plan, (int)c.M, c.R, c.n);
 }
 
 // A launch of clusters of (x, 1, 1) CTAs; `dependent`: it may start while the previous kernel drains.
@@ -1004,8 +1005,7 @@ cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, f
     const int tiles = tiles_at_most(c);
     const int psplits = stage_splits(c.K, tiles, 296, kPortableCluster), usplits = stage_splits(c.N, tiles, 296, 1 << 20);
     const Products p{(const bf16*)X, (const bf16*)c.A, c.scale, H, (bf16*)w.packed_g, (int)c.K, c.R, false};
-    // update_kernel reads B before it waits: what widened it has to be over when the products start
-    e = launch_clusters(pfn, dim3((unsigned)psplits, (unsigned)tiles), psplits, SP::smem, false, st, p, c.plan, (int)c.M, c.R, c.n);
+    e = launch_clusters(pfn, dim3((unsigned)psplits, (unsigned)tiles), psplits, SP::smem, true, st, p, c.plan, (int)c.M, c.R, c.n);
     if (e != cudaSuccess) return e;
     const Update d{(const bf16*)w.packed_g, (const bf16*)B, (const bf16*)Y, (bf16*)out, (int)c.N, ld, usplits};
     return launch_dependent(ufn, dim3((unsigned)usplits, (unsigned)tiles), dim3(kThreads), SU::smem, st, d, c.plan, (int)c.M, c.R, c.n);

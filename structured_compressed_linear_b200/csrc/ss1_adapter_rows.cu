@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const T* __restrict__ X,
                                                         const int32_t* __restrict__ index, const float* __restrict__ scale,
                                                         const T* Y, T* out, float* __restrict__ H, int M, int K, int N, int R, int n) {
     __shared__ float part[kMaxRank], h[kMaxRank];
+    wait_for_previous();
+    let_next_start();
     const int m = blockIdx.y, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int rank = blockIdx.x % kCluster, groups = gridDim.x / kCluster, group = blockIdx.x / kCluster;
     const int a = index ? index[m] : 0;
@@ -124,13 +126,15 @@ cudaError_t launch(const Call& c, const void* X, const void* Y, void* out, float
     cfg.gridDim = dim3((unsigned)(kCluster * groups), (unsigned)c.M);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, &rows_kernel<T>, (const T*)X, (const T*)c.A, (const T*)c.B, c.index, c.scale, (const T*)Y, (T*)out, H,
                               (int)c.M, (int)c.K, (int)c.N, c.R, c.n);
 }

@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
                                                                              int64_t M, int K, float eps) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float buf[2][32];
+    wait_for_previous();
+    let_next_start();
     constexpr bool kRing = in_ring<T, VEC>(), kShared = WARP && VEC;
     constexpr int kDepth = fwd_ahead<T>(NU, THREADS), kPlace = unit_bytes<T>() * THREADS, kRow = NU * kPlace;
     __shared__ __align__(16) float weights[kShared ? 2 : 1][kShared ? NU * 2 : 1][kShared ? 128 : 4];   // [w, b][half unit][lane * 4]
@@ -319,8 +321,8 @@ cudaError_t fwd_launch(const void* X, const void* w, const void* b, void* Y, flo
         if (e != cudaSuccess) return e;
     }
     const int64_t rows = WARP ? threads / 32 : 1, need = (M + rows - 1) / rows, most = 148 * fwd_ctas(THREADS);
-    fn<<<(unsigned)(need < most ? need : most), threads, smem, st>>>((const T*)X, (const W*)w, (const W*)b, (T*)Y, mean, rstd, M, K, eps);
-    return cudaGetLastError();
+    return launch_dependent(fn, dim3((unsigned)(need < most ? need : most)), dim3((unsigned)threads), smem, st, (const T*)X, (const W*)w,
+                            (const W*)b, (T*)Y, mean, rstd, M, K, eps);
 }
 
 // Widest row of the register kernels: 1024 threads of four units.
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
     __shared__ __align__(16) float4 buf[2][15][16];             // a row's two sums of each warp, for two rows
     constexpr bool kRing = in_ring<T, VEC>();
     constexpr int kDepth = bwd_ahead<T>(), kPlace = unit_bytes<T>() * kBwdThreads, kTurn = 4 * kPlace;
+    wait_for_previous();
     let_next_start();
     const int g = threadIdx.x / width, t = threadIdx.x % width, warps = width / 32, warp = t / 32;
     for (int i = threadIdx.x; i < 2 * 15 * 16; i += blockDim.x) (&buf[0][0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -612,8 +615,8 @@ cudaError_t bwd_rows(const void* dY, const void* X, const float* mean, const flo
     constexpr int turns = in_ring<T, VEC>() ? bwd_ahead<T>() * 4 * unit_bytes<T>() * kBwdThreads : 0, smem = turns > most_sums ? turns : most_sums;
     const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return e;
-    fn<<<(unsigned)ctas, width * groups, smem, st>>>((const T*)dY, (const T*)X, mean, rstd, (const W*)w, (T*)dX, part, M, K, width, groups);
-    return cudaGetLastError();
+    return launch_dependent(fn, dim3((unsigned)ctas), dim3((unsigned)(width * groups)), smem, st, (const T*)dY, (const T*)X, mean, rstd,
+                            (const W*)w, (T*)dX, part, M, K, width, groups);
 }
 
 template <typename T, typename W, bool VEC>

@@ -141,8 +141,10 @@ inline size_t dtype_size(int dtype) { return dtype == SS1_DTYPE_BF16 ? 2 : 4; }
 inline bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 // Launches `kernel` so that it may start while the previous kernel on the stream drains
-// (programmatic dependent launch); the kernel waits with griddepcontrol.wait before it reads
-// what that kernel wrote.
+// (programmatic dependent launch). Rules that every kernel launched like this keeps: all its CTAs execute
+// griddepcontrol.wait before they end, so that what it has waited for is over for whoever waits for it; and
+// before the wait it touches nothing that an earlier kernel may still write. A kernel lets its
+// successor start only after its own wait, except where its successor waits first thing.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
