@@ -18,6 +18,7 @@
 // The plan lists the rows by adapter (stable, so sums over an adapter's rows have one order), and
 // tiles of up to kTile rows of one adapter.
 #include "ss1_adapter.cuh"
+#include "ptx_sm100.cuh"
 
 namespace ss1 {
 namespace ada {
@@ -168,6 +169,11 @@ cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, c
 
 namespace {
 
+int64_t sub_tiles(const Call& c) {
+    const int64_t tiles = c.plan.rows ? c.plan.max_tiles : (c.M + kTile - 1) / kTile;
+    return tiles * (kTile / 32);
+}
+
 // ---- general path: any type, size and alignment, on the CUDA cores -----------------------------
 
 constexpr int kRanks = 16;   // ranks a thread sums at a time
@@ -225,8 +231,7 @@ __global__ void __launch_bounds__(256) row_update_kernel(const float* __restrict
                                                          const T* in, T* out, int64_t M, int C, int R, int n, int cs, int rs,
                                                          int site_t) {
     __shared__ float p[kMaxRank];
-    const int64_t m = blockIdx.y + (int64_t)blockIdx.z * 65535;
-    if (m >= M) return;
+    const int64_t m = blockIdx.y;
     const int a = index ? index[m] : 0;
     const bool some = (unsigned)a < (unsigned)n;
     const float f = some && scale ? scale[a] : 1.0f;
@@ -249,29 +254,249 @@ __global__ void __launch_bounds__(256) row_update_kernel(const float* __restrict
     }
 }
 
+// The same three sums for more rows, with rows of one adapter together: each element of a table or of P that is
+// read serves many rows or columns. A sub-tile is 32 rows of one of the plan's tiles.
+constexpr int kSub = 32, kSubs = kTile / kSub;
+constexpr int kWide = 128;    // columns of a stage
+
+struct SubTile {
+    int adapter, first, rows;
+};
+__device__ __forceinline__ SubTile sub_tile(const PlanView& plan, int i, int M, int n) {
+    SubTile t{0, i / kSubs * kTile, min(kTile, M - i / kSubs * kTile)};
+    if (plan.rows) {
+        const int4 p = plan.tiles[i / kSubs];
+        t = SubTile{p.x < n ? p.x : -1, p.y, p.y < 0 ? 0 : min(p.z, min(kTile, M - p.y))};
+    }
+    t.first += i % kSubs * kSub;
+    t.rows = min(kSub, t.rows - i % kSubs * kSub);
+    return t;
+}
+__device__ __forceinline__ int64_t plan_row(const PlanView& plan, int place, int M) {
+    const int m = plan.rows ? plan.rows[place] : place;
+    return (unsigned)m < (unsigned)M ? m : -1;
+}
+
+// P of a sub-tile and kRanks ranks a CTA. Stages of kWide columns of U and the table in shared memory as float; a lane is
+// a row, a warp takes every eighth column and sums all ranks (16 multiply-adds for five shared-memory
+// reads); the warps' sums meet at the end. The next stage's elements are loaded before this one's sums. Where
+// the sub-tiles are few, a cluster's CTAs share the columns and their sums meet in distributed shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256) tile_products_kernel(const T* __restrict__ U, const T* __restrict__ table, PlanView plan,
+                                                            const float* __restrict__ scale, float* __restrict__ P, int M, int C, int R,
+                                                            int n, int cs, int rs, int splits, int site_u, int site_t) {
+    __shared__ float u[kSub][kWide + 1];
+    __shared__ __align__(16) float t[kWide][kRanks];
+    __shared__ float part[8][kRanks][kSub + 1];
+    float* sums = &u[0][0];                    // once the last stage is over
+    __shared__ int64_t rows[kSub];
+    const SubTile tile = sub_tile(plan, blockIdx.x / splits, M, n);
+    if (tile.rows <= 0) return;                // the whole cluster, here and below
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, split = blockIdx.x % splits;
+    const int stages = (C + kWide - 1) / kWide, per = (stages + splits - 1) / splits;
+    const int from = min(C, split * per * kWide), to = min(C, from + per * kWide);
+    const int r0 = blockIdx.y * kRanks, ranks = min(kRanks, R - r0);
+    if (tid < kSub) rows[tid] = tid < tile.rows ? plan_row(plan, tile.first + tid, M) : -1;
+    __syncthreads();
+    if (tile.adapter < 0) {        // rows without an adapter
+        for (int i = split * 256 + tid; i < tile.rows * ranks; i += splits * 256) {
+            const int64_t m = rows[i / ranks];
+            if (m >= 0 && SS1_IN(m * R + r0 + i % ranks, (int64_t)M * R, kSiteAdaH)) P[m * R + r0 + i % ranks] = 0.0f;
+        }
+        return;
+    }
+    const int64_t base = (int64_t)tile.adapter * C * R;
+    [[maybe_unused]] const int64_t tsize = (int64_t)n * C * R;
+    // this thread's elements of a stage: of U a column of every second row, of the table along its contiguous side
+    constexpr int kMyU = kSub * kWide / 256, kMyT = kWide * kRanks / 256, kStep = 256 / kWide;
+    const int uc = tid % kWide, ur = tid / kWide;
+    int tc[kMyT], tr[kMyT];
+#pragma unroll
+    for (int i = 0; i < kMyT; ++i) {
+        const int e = tid + i * 256;
+        tc[i] = rs == 1 ? e / kRanks : e % kWide;
+        tr[i] = rs == 1 ? e % kRanks : e / kWide;
+    }
+    T nu[kMyU], nt[kMyT];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kMyU; ++i) {
+            const int64_t m = rows[ur + kStep * i];
+            nu[i] = m >= 0 && c0 + uc < C && SS1_IN(m * C + c0 + uc, (int64_t)M * C, site_u) ? U[m * C + c0 + uc] : from_f<T>(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kMyT; ++i) {
+            const int64_t at = base + (int64_t)(c0 + tc[i]) * cs + (int64_t)(r0 + tr[i]) * rs;
+            nt[i] = tr[i] < ranks && c0 + tc[i] < C && SS1_IN(at, tsize, site_t) ? table[at] : from_f<T>(0.0f);
+        }
+    };
+    float s[kRanks];
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r) s[r] = 0.0f;
+    fetch(from);
+    for (int c0 = from; c0 < to; c0 += kWide) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMyU; ++i) u[ur + kStep * i][uc] = to_f(nu[i]);
+#pragma unroll
+        for (int i = 0; i < kMyT; ++i) t[tc[i]][tr[i]] = to_f(nt[i]);
+        __syncthreads();
+        if (c0 + kWide < to) fetch(c0 + kWide);
+#pragma unroll
+        for (int k = 0; k < kWide / 8; ++k) {
+            const int c = k * 8 + warp;
+            const float x = u[lane][c];
+            const float4* row = reinterpret_cast<const float4*>(t[c]);
+#pragma unroll
+            for (int r = 0; r < kRanks / 4; ++r) {
+                const float4 v = row[r];
+                s[4 * r] = fmaf(x, v.x, s[4 * r]);
+                s[4 * r + 1] = fmaf(x, v.y, s[4 * r + 1]);
+                s[4 * r + 2] = fmaf(x, v.z, s[4 * r + 2]);
+                s[4 * r + 3] = fmaf(x, v.w, s[4 * r + 3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r) part[warp][r][lane] = s[r];
+    __syncthreads();
+    const float f = scale ? scale[tile.adapter] : 1.0f;
+    for (int i = tid; i < kSub * kRanks; i += 256) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += part[w][i % kRanks][i / kRanks];
+        sums[i] = v;
+    }
+    if (splits > 1) ptx::cluster_sync();
+    else __syncthreads();
+    for (int i = split * 256 + tid; i < kSub * kRanks; i += splits * 256) {
+        const int r = i % kRanks;
+        float v = 0.0f;
+        if (splits > 1)
+            for (int k = 0; k < splits; ++k) v += ptx::ld_cluster_f32(ptx::map_to_rank(sums + i, k));
+        else
+            v = sums[i];
+        const int64_t m = rows[i / kRanks];
+        if (m >= 0 && r < ranks && SS1_IN(m * R + r0 + r, (int64_t)M * R, kSiteAdaH)) P[m * R + r0 + r] = f * v;
+    }
+    if (splits > 1) ptx::cluster_sync();       // nobody leaves while its sums are being read
+}
+
+// out of `subs` sub-tiles of a tile and 256 columns: a thread is a column, its table row in registers kRanks at a time
+// (and kept for all of them where R is no more), P's rows in shared memory, 32 rows at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) tile_update_kernel(const float* __restrict__ P, const T* __restrict__ table, PlanView plan,
+                                                          const float* __restrict__ scale, const T* in, T* out, int M, int C, int R, int n,
+                                                          int cs, int rs, int subs, int site_t) {
+    __shared__ __align__(16) float p[kSub][kRanks];
+    __shared__ int64_t rows[kSub];
+    const int cols = (C + 255) / 256;      // CTAs side by side
+    const int tid = threadIdx.x, c = blockIdx.x % cols * 256 + tid;
+    [[maybe_unused]] const int64_t total = (int64_t)M * C, tsize = (int64_t)n * C * R;
+    float w[kRanks];
+    for (int sub = 0; sub < subs; ++sub) {      // 1, or all of a tile's
+        const SubTile tile = sub_tile(plan, blockIdx.x / cols * subs + sub, M, n);
+        if (tile.rows <= 0) return;
+        __syncthreads();
+        if (tid < kSub) rows[tid] = tid < tile.rows ? plan_row(plan, tile.first + tid, M) : -1;
+        __syncthreads();
+        if (tile.adapter < 0) {
+            if (in == out) return;
+            T v[kSub];
+#pragma unroll
+            for (int i = 0; i < kSub; ++i)
+                v[i] = in && c < C && rows[i] >= 0 && SS1_IN(rows[i] * C + c, total, kSiteAdaY) ? in[rows[i] * C + c] : from_f<T>(0.0f);
+#pragma unroll
+            for (int i = 0; i < kSub; ++i)
+                if (c < C && rows[i] >= 0 && SS1_IN(rows[i] * C + c, total, kSiteAdaY)) out[rows[i] * C + c] = v[i];
+            continue;
+        }
+        const float f = scale ? scale[tile.adapter] : 1.0f;
+        const int64_t base = (int64_t)tile.adapter * C * R + (int64_t)c * cs;
+        float v[kSub];
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+            v[i] = in && c < C && rows[i] >= 0 && SS1_IN(rows[i] * C + c, total, kSiteAdaY) ? to_f(in[rows[i] * C + c]) : 0.0f;
+        for (int r0 = 0; r0 < R; r0 += kRanks) {
+            if (r0 > 0) __syncthreads();
+            for (int i = tid; i < kSub * kRanks; i += 256) {
+                const int64_t m = rows[i / kRanks];
+                const int r = r0 + i % kRanks;
+                p[i / kRanks][i % kRanks] = m >= 0 && r < R ? f * P[m * R + r] : 0.0f;
+            }
+            if (R > kRanks || sub == 0) {
+#pragma unroll
+                for (int r = 0; r < kRanks; ++r) {
+                    const int64_t at = base + (int64_t)(r0 + r) * rs;
+                    w[r] = c < C && r0 + r < R && SS1_IN(at, tsize, site_t) ? to_f(table[at]) : 0.0f;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+                const float4* row = reinterpret_cast<const float4*>(p[i]);
+#pragma unroll
+                for (int r = 0; r < kRanks / 4; ++r) {
+                    const float4 x = row[r];
+                    v[i] = fmaf(x.x, w[4 * r], v[i]);
+                    v[i] = fmaf(x.y, w[4 * r + 1], v[i]);
+                    v[i] = fmaf(x.z, w[4 * r + 2], v[i]);
+                    v[i] = fmaf(x.w, w[4 * r + 3], v[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+            if (c < C && rows[i] >= 0 && SS1_IN(rows[i] * C + c, total, kSiteAdaY)) out[rows[i] * C + c] = from_f<T>(v[i]);
+    }
+}
+
 // D_a[c, r] = f * sum over adapter a's rows of U[m, c] P[m, r], for one share of the rows (blockIdx.z):
-// element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs.
+// element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs. A thread is a column; 32 rows' P
+// lie in shared memory, and 32 rows of U are on their way at a time.
 template <typename T>
 __global__ void __launch_bounds__(128) column_sums_kernel(const T* __restrict__ U, const float* __restrict__ P, PlanView plan,
                                                           const float* __restrict__ scale, float* __restrict__ D, int64_t M,
                                                           int C, int R, int n, int cs, int rs, int site_u) {
+    __shared__ __align__(16) float p[kSub][kRanks];
+    __shared__ int64_t rows[kSub];
     const int a = blockIdx.y % n, r0 = (blockIdx.y / n) * kRanks, ranks = min(kRanks, R - r0);
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= C) return;
-    const int begin = plan.rows ? plan.first[a] : 0, end = plan.rows ? plan.first[a + 1] : (int)M;
-    const int shares = gridDim.z, per = (end - begin + shares - 1) / shares;
+    const int begin = plan.rows ? max(0, plan.first[a]) : 0, end = plan.rows ? min((int)M, plan.first[a + 1]) : (int)M;
+    const int shares = gridDim.z, per = (max(0, end - begin) + shares - 1) / shares;
     const int from = begin + (int)blockIdx.z * per, to = min(end, from + per);
     float s[kRanks];
 #pragma unroll
     for (int r = 0; r < kRanks; ++r) s[r] = 0.0f;
-    for (int i = from; i < to; ++i) {
-        const int64_t m = plan.rows ? plan.rows[i] : i;
-        if ((uint64_t)m >= (uint64_t)M || !SS1_IN(m * C + c, M * C, site_u)) continue;
-        const float u = to_f(U[m * C + c]);
+    for (int at = from; at < to; at += kSub) {
+        __syncthreads();
+        if (threadIdx.x < kSub) rows[threadIdx.x] = at + (int)threadIdx.x < to ? plan_row(plan, at + threadIdx.x, (int)M) : -1;
+        __syncthreads();
+        T u[kSub];
 #pragma unroll
-        for (int r = 0; r < kRanks; ++r)
-            if (r < ranks) s[r] = fmaf(u, P[m * R + r0 + r], s[r]);
+        for (int i = 0; i < kSub; ++i)
+            u[i] = rows[i] >= 0 && c < C && SS1_IN(rows[i] * C + c, M * C, site_u) ? U[rows[i] * C + c] : from_f<T>(0.0f);
+        for (int i = threadIdx.x; i < kSub * kRanks; i += 128) {
+            const int64_t m = rows[i / kRanks];
+            const int r = i % kRanks;
+            p[i / kRanks][r] = m >= 0 && r < ranks ? P[m * R + r0 + r] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) {
+            const float x = to_f(u[i]);
+            const float4* row = reinterpret_cast<const float4*>(p[i]);
+#pragma unroll
+            for (int r = 0; r < kRanks / 4; ++r) {
+                const float4 v = row[r];
+                s[4 * r] = fmaf(x, v.x, s[4 * r]);
+                s[4 * r + 1] = fmaf(x, v.y, s[4 * r + 1]);
+                s[4 * r + 2] = fmaf(x, v.z, s[4 * r + 2]);
+                s[4 * r + 3] = fmaf(x, v.w, s[4 * r + 3]);
+            }
+        }
     }
+    if (c >= C) return;
     const float f = scale ? scale[a] : 1.0f;
     const int64_t size = (int64_t)n * C * R;
     const int64_t base = (int64_t)blockIdx.z * size + (int64_t)a * C * R + (int64_t)c * cs;
@@ -291,15 +516,67 @@ __global__ void __launch_bounds__(256) add_shares_kernel(const float* __restrict
     out[i] = from_f<T>(s);
 }
 
+// A CTA takes one row while that reads no more than kAloneWork elements of A and B; beyond, 32 rows of an adapter
+// together, with a plan. Measured forward, us, a row / 32 rows: float32 333 x 1001 x 770, rank 6 (3.5 M elements) 9.9 / 16.6;
+// 200 x 1024 x 1024, rank 16 (6.5 M) 14.7 / 16.6; bf16 200 x 3001 x 5001, rank 16 (26 M) 31 / 25; float32
+// 1024 x 1024 x 1024, rank 16 (34 M) 46 / 13.
+constexpr int64_t kAloneWork = 1 << 23;
+bool alone(const Call& c) { return c.M <= 65535 && c.M * c.R * (c.K + c.N) <= kAloneWork; }
+
+// P[m] = f U[m] T_a and out[m] = in[m] + f P[m] T_a, whichever way suits the rows.
+template <typename T>
+cudaError_t products(const Call& c, const void* U, const void* table, const float* scale, float* P, int64_t C, int cs, int rs, int site_u,
+                     int site_t, cudaStream_t st) {
+    const unsigned ranks = (unsigned)((c.R + kRanks - 1) / kRanks);
+    if (alone(c))
+        row_products_kernel<T><<<dim3((unsigned)c.M, ranks), 256, 0, st>>>((const T*)U, (const T*)table, c.index, scale, P, c.M, (int)C, c.R,
+                                                                          c.n, cs, rs, site_u, site_t);
+    else {
+        // two CTAs for each of 148 SMs, at least two stages each, clusters of a portable size
+        const int64_t subs = sub_tiles(c), stages = (C + kWide - 1) / kWide;
+        int64_t splits = 296 / (subs * ranks);
+        splits = splits > stages / 2 ? stages / 2 : splits;
+        splits = splits > 8 ? 8 : (splits < 1 ? 1 : splits);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(subs * splits), ranks);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)splits;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, &tile_products_kernel<T>, (const T*)U, (const T*)table, c.plan, scale, P, (int)c.M, (int)C, c.R, c.n,
+                                  cs, rs, (int)splits, site_u, site_t);
+    }
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t update(const Call& c, const float* P, const void* table, const float* scale, const void* in, void* out, int64_t C, int cs, int rs,
+                   int site_t, cudaStream_t st) {
+    const unsigned cols = (unsigned)((C + 255) / 256);
+    if (alone(c))
+        row_update_kernel<T><<<dim3(cols, (unsigned)c.M), 256, 0, st>>>(P, (const T*)table, c.index, scale, (const T*)in, (T*)out, c.M, (int)C,
+                                                                       c.R, c.n, cs, rs, site_t);
+    else {
+        // a whole tile a CTA (its table row read once) where that still gives eight CTAs for each of 148 SMs: bf16
+        // 4000 x 4001 x 4003, rank 16, 134 us against 147; 32 rows a CTA elsewhere: float32 1024 x 1024 x 1024 13 against 25
+        const int subs = sub_tiles(c) / kSubs * cols >= 148 * 8 ? kSubs : 1;
+        const int64_t ctas = sub_tiles(c) / subs * cols;
+        if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        tile_update_kernel<T><<<(unsigned)ctas, 256, 0, st>>>(P, (const T*)table, c.plan, scale, (const T*)in, (T*)out, (int)c.M, (int)C, c.R,
+                                                             c.n, cs, rs, subs, site_t);
+    }
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t forward_general(const Call& c, const void* X, const void* Y, void* out, float* H, cudaStream_t st) {
-    const dim3 grid((unsigned)c.M, (unsigned)((c.R + kRanks - 1) / kRanks));
-    row_products_kernel<T><<<grid, 256, 0, st>>>((const T*)X, (const T*)c.A, c.index, nullptr, H, c.M, (int)c.K, c.R, c.n, 1,
-                                                 (int)c.K, kSiteAdaX, kSiteAdaA);
-    const dim3 egrid((unsigned)((c.N + 255) / 256), (unsigned)(c.M < 65535 ? c.M : 65535), (unsigned)((c.M + 65534) / 65535));
-    row_update_kernel<T><<<egrid, 256, 0, st>>>(H, (const T*)c.B, c.index, c.scale, (const T*)Y, (T*)out, c.M, (int)c.N, c.R, c.n,
-                                                c.R, 1, kSiteAdaB);
-    return cudaGetLastError();
+    const cudaError_t e = products<T>(c, X, c.A, nullptr, H, c.K, 1, (int)c.K, kSiteAdaX, kSiteAdaA, st);
+    if (e != cudaSuccess) return e;
+    return update<T>(c, H, c.B, c.scale, Y, out, c.N, c.R, 1, kSiteAdaB, st);
 }
 
 template <typename T>
@@ -317,18 +594,8 @@ template <typename T>
 cudaError_t backward_general(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX,
                              void* dA, void* dB, float* G, float* part, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (dX || dA) {
-        const dim3 grid((unsigned)c.M, (unsigned)((c.R + kRanks - 1) / kRanks));
-        row_products_kernel<T><<<grid, 256, 0, st>>>((const T*)dY, (const T*)c.B, c.index, c.scale, G, c.M, (int)c.N, c.R, c.n, c.R,
-                                                     1, kSiteAdaY, kSiteAdaB);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && dX) {
-        const dim3 grid((unsigned)((c.K + 255) / 256), (unsigned)(c.M < 65535 ? c.M : 65535), (unsigned)((c.M + 65534) / 65535));
-        row_update_kernel<T><<<grid, 256, 0, st>>>(G, (const T*)c.A, c.index, nullptr, (const T*)dX_in, (T*)dX, c.M, (int)c.K, c.R,
-                                                   c.n, 1, (int)c.K, kSiteAdaA);
-        e = cudaGetLastError();
-    }
+    if (dX || dA) e = products<T>(c, dY, c.B, c.scale, G, c.N, c.R, 1, kSiteAdaY, kSiteAdaB, st);
+    if (e == cudaSuccess && dX) e = update<T>(c, G, c.A, nullptr, dX_in, dX, c.K, 1, (int)c.K, kSiteAdaA, st);
     if (e == cudaSuccess && dA) e = column_sums<T>(c, X, G, nullptr, dA, part, c.K, 1, (int)c.K, kSiteAdaX, st);
     if (e == cudaSuccess && dB) e = column_sums<T>(c, dY, H, c.scale, dB, part, c.N, c.R, 1, kSiteAdaY, st);
     return e;
@@ -497,7 +764,9 @@ extern "C" SS1_API int ss1_adapter_forward(const ss1_adapters* ad, const void* X
         return SS1_OK;
     }
     if (!H) H = reinterpret_cast<float*>(ws + s.plan);
-    err = ad->dtype == SS1_DTYPE_BF16 ? forward_general<__nv_bfloat16>(c, X, Y, out, H, st)
+    if (!alone(c)) err = plan_of(*ad, M, ws, c, st);
+    if (err == cudaSuccess)
+        err = ad->dtype == SS1_DTYPE_BF16 ? forward_general<__nv_bfloat16>(c, X, Y, out, H, st)
                                                         : forward_general<float>(c, X, Y, out, H, st);
     if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
     return SS1_OK;
