@@ -3,7 +3,9 @@
 The arithmetic runs in the CUDA library (include/ss1.h); this module checks tensors, allocates
 outputs and workspaces, and passes pointers, sizes and the stream. Every call runs on the device
 of its tensors, on `stream` or that device's current stream, and never falls back to another
-implementation. Tensors are contiguous CUDA tensors, bf16 or float32.
+implementation. Tensors are contiguous CUDA tensors, bf16 or float32. For a CUDA graph, capture these
+functions; a backward pass through autograd is captured only while no eager graph of the same leaves
+is alive (autograd ties a leaf to the stream of its first use).
 """
 
 from __future__ import annotations
@@ -44,18 +46,9 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr() if t is not None else None
 
 
-def _call(device: int, stream: Optional[torch.cuda.Stream], made, fn, *args):
-    """fn(*args, stream handle) on `device` (made current for the call where it is not); on a stream other
-    than the one that they came from, `made` (tensors that this module allocated) are tied to it."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        if stream.device.index != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
-        handle = stream.cuda_stream
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _call(device: int, fn, *args):
+    """fn(*args, the device's current stream) on `device`, made current for the call where it is not."""
+    handle = torch._C._cuda_getCurrentRawStream(device)
     if torch._C._cuda_getDevice() == device:
         status = fn(*args, handle)
     else:
@@ -63,6 +56,21 @@ def _call(device: int, stream: Optional[torch.cuda.Stream], made, fn, *args):
             status = fn(*args, handle)
     if status != 0:
         _check(status, fn.__name__)
+
+
+def _streamed(fn):
+    """Adds the argument `stream`: the call, and what it allocates, then belong to that stream. (Memory that another
+    stream's allocator handed out could still be in use there.)"""
+    @functools.wraps(fn)
+    def call(first, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        if stream is None:
+            return fn(first, *args, **kw)
+        t = first[0] if isinstance(first, (list, tuple)) and first else first
+        if isinstance(t, torch.Tensor) and t.device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
 
 
 def _apart(out: torch.Tensor, name: str, **inputs):
@@ -103,9 +111,9 @@ def _norm_workspace(L, M: int, K: int) -> int:
     return n.value
 
 
+@_streamed
 def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-                      eps: float = 1e-5, out: Optional[torch.Tensor] = None,
-                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                      eps: float = 1e-5, out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(Y, mean, rstd) of X [M, K]: Y in X's dtype, mean and rstd float32 [M] (ss1_layernorm_forward).
     weight and bias [K] in X's dtype, or float32 beside bf16 rows."""
     M, K = _norm_rows(X)
@@ -117,14 +125,14 @@ def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bi
         Y = _tensor("out", out, X.shape, X.dtype, device)
         _apart(Y, "out", X=X, weight=weight, bias=bias)
     mean, rstd = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
-    _call(device, stream, (Y if out is None else None, mean, rstd), lib().ss1_layernorm_forward, X.data_ptr(), _ptr(weight),
+    _call(device, lib().ss1_layernorm_forward, X.data_ptr(), _ptr(weight),
           _ptr(bias), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), M, K, eps, _dtype_code(X.dtype), _dtype_code(wt))
     return Y, mean, rstd
 
 
+@_streamed
 def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
-                       weight: Optional[torch.Tensor] = None, need: Tuple[bool, bool, bool] = (True, True, True),
-                       stream: Optional[torch.cuda.Stream] = None):
+                       weight: Optional[torch.Tensor] = None, need: Tuple[bool, bool, bool] = (True, True, True)):
     """(dX, dweight, dbias) from dY, the forward's X, mean and rstd (ss1_layernorm_backward). dweight and
     dbias have weight's dtype (X's without a weight). `need`: which of the three to compute (the
     others are None)."""
@@ -140,7 +148,7 @@ def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rs
     db = X.new_empty(K, dtype=wt) if need[2] else None
     size = _norm_workspace(L, M, K) if need[1] or need[2] else 0
     ws = X.new_empty(size, dtype=torch.uint8) if size else None
-    _call(device, stream, (dX, dw, db, ws), L.ss1_layernorm_backward, dY.data_ptr(), X.data_ptr(), mean.data_ptr(),
+    _call(device, L.ss1_layernorm_backward, dY.data_ptr(), X.data_ptr(), mean.data_ptr(),
           rstd.data_ptr(), _ptr(weight), _ptr(dX), _ptr(dw), _ptr(db), M, K, _dtype_code(X.dtype), _dtype_code(wt), _ptr(ws),
           size)
     return dX, dw, db
@@ -186,7 +194,8 @@ def _plan_bytes(L, M: int, count: int) -> int:
     return n.value
 
 
-def adapter_plan(index: torch.Tensor, count: int, stream: Optional[torch.cuda.Stream] = None) -> AdapterPlan:
+@_streamed
+def adapter_plan(index: torch.Tensor, count: int) -> AdapterPlan:
     """Plan of `index` (int32 [M]; outside [0, count): no adapter) for adapter_forward and adapter_backward."""
     _tensor("index", index, dtype=torch.int32)
     if index.dim() != 1:
@@ -194,7 +203,7 @@ def adapter_plan(index: torch.Tensor, count: int, stream: Optional[torch.cuda.St
     M, L = index.shape[0], lib()
     size = _plan_bytes(L, M, count)
     data = index.new_empty(size, dtype=torch.uint8)
-    _call(index.get_device(), stream, (data,), L.ss1_adapter_plan, index.data_ptr(), M, count, data.data_ptr(), size)
+    _call(index.get_device(), L.ss1_adapter_plan, index.data_ptr(), M, count, data.data_ptr(), size)
     return AdapterPlan(data, M, count)
 
 
@@ -233,18 +242,18 @@ def _adapters(X, A, B, index, scale, plan):
     return device, M, K, N, R, packed, code, n
 
 
+@_streamed
 def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.Tensor, index: Optional[torch.Tensor] = None,
                     scale: Optional[torch.Tensor] = None, keep: bool = False, plan: Optional[AdapterPlan] = None,
-                    out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+                    out: Optional[torch.Tensor] = None):
     """Y[m] + scale[a] (X[m] A[a]^T) B[a]^T with a = index[m] (ss1_adapter_forward): X [M, K] and the
     projection's output Y [M, N], A [count, R, K], B [count, N, R], scale float32 [count]. index int32
     [M]; an entry outside [0, count) leaves its row as it is; None: every row uses the one adapter.
     `out` may be Y itself. keep: returns (out, H) with H = X A^T, float32 [M, R], for the backward pass."""
     device, M, K, N, R, ad, code, n = _adapters(X, A, B, index, scale, plan)
     _tensor("Y", Y, (M, N), X.dtype, device)
-    own = None
     if out is None:
-        out = own = torch.empty_like(Y)
+        out = torch.empty_like(Y)
     else:
         _tensor("out", out, Y.shape, Y.dtype, device)
         _apart(out, "out", X=X, A=A, B=B, Y=Y if out.data_ptr() != Y.data_ptr() else None)
@@ -252,15 +261,16 @@ def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.
     L = lib()
     size = _adapter_workspace(L, M, K, N, R, n, code, False)
     ws = X.new_empty(size, dtype=torch.uint8)
-    _call(device, stream, (own, H, ws), L.ss1_adapter_forward, ad, X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
+    _call(device, L.ss1_adapter_forward, ad, X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
           ws.data_ptr(), size)
     return (out, H) if keep else out
 
 
+@_streamed
 def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, H: Optional[torch.Tensor],
                      dX: Optional[torch.Tensor] = None, index: Optional[torch.Tensor] = None,
                      scale: Optional[torch.Tensor] = None, plan: Optional[AdapterPlan] = None,
-                     need: Tuple[bool, bool, bool] = (True, True, True), stream: Optional[torch.cuda.Stream] = None):
+                     need: Tuple[bool, bool, bool] = (True, True, True)):
     """(dX, dA, dB) of adapter_forward for dY, the gradient of its output (ss1_adapter_backward). H is what
     the forward kept (needed for dB); `dX`, if given, is the projection's input gradient, which the
     result includes. `need`: which of the three to compute (the others are None)."""
@@ -278,7 +288,7 @@ def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torc
     L = lib()
     size = _adapter_workspace(L, M, K, N, R, n, code, True)
     ws = X.new_empty(size, dtype=torch.uint8)
-    _call(device, stream, (out, dA, dB, ws), L.ss1_adapter_backward, ad, dY.data_ptr(), X.data_ptr(),
+    _call(device, L.ss1_adapter_backward, ad, dY.data_ptr(), X.data_ptr(),
           H.data_ptr() if need[2] else None, _ptr(dX) if need[0] else None, _ptr(out), _ptr(dA), _ptr(dB), M, ws.data_ptr(), size)
     return out, dA, dB
 
@@ -350,12 +360,13 @@ def _like(name: str, ts: Sequence[torch.Tensor], sizes: List[int], device: int, 
 _WEIGHTS, _F32, _U8 = {torch.bfloat16, torch.float32}, {torch.float32}, {torch.uint8}
 
 
+@_streamed
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor],
                exp_avg_sq: Sequence[torch.Tensor], step: int = 1, lr: float = 1e-3,
                betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                grad_scale: float = 1.0, master: Optional[Sequence[Optional[torch.Tensor]]] = None,
                scales: Optional[Tuple[Sequence[torch.Tensor], Sequence[torch.Tensor]]] = None,
-               factors: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+               factors: Optional[torch.Tensor] = None) -> None:
     """One AdamW step over all tensors, in place (ss1_adamw_step). params and grads: bf16 or float32, each
     tensor by itself. exp_avg and exp_avg_sq: float32; with `scales` = (of the first moment, of the
     root of the second one), float32 [ceil(numel / ADAMW_BLOCK)] each, uint8 E4M3 codes instead.
@@ -370,7 +381,10 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     bits = 32 if scales is None else 8
     sizes = list(map(_NUMEL, params))
     table = np.zeros(n, _ADAMW_TENSOR)
-    table["param"] = _like("params", params, sizes, device, _WEIGHTS)
+    where = _like("params", params, sizes, device, _WEIGHTS)
+    if len(set(where)) < n and len({p for p, size in zip(where, sizes) if size}) < sum(size > 0 for size in sizes):
+        raise ValueError("a parameter is in the list twice")
+    table["param"] = where
     table["grad"] = _like("grads", grads, sizes, device, _WEIGHTS)
     state = _F32 if bits == 32 else _U8
     table["exp_avg"] = _like("exp_avg", exp_avg, sizes, device, state)
@@ -394,7 +408,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     if factors is not None:
         _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
     hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
-    _call(device, stream, (), lib().ss1_adamw_step, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors))
+    _call(device, lib().ss1_adamw_step, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors))
 
 
 class AdamW:
@@ -438,7 +452,7 @@ class AdamW:
             return [ts[i] for i in who]
         adamw_step(of(self.params), [self.params[i].grad for i in who], of(self.exp_avg), of(self.exp_avg_sq),
                    self.steps + 1, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, of(self.master),
-                   None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors, stream)
+                   None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors, stream=stream)
         self.steps += 1
 
     def state_dict(self) -> dict:

@@ -287,8 +287,26 @@ def test_refusals_change_nothing(ops):
                 lambda: ops.adamw_step([P], [G.half()], [M], [V]), lambda: ops.adamw_step([P], [G.cpu()], [M], [V]),
                 lambda: ops.adamw_step([P], [G], [M], [V], master=[M[::2]]), lambda: ops.adamw_step([P], [G], [M], [V], betas=(1.0, 0.9)),
                 lambda: ops.adamw_step([P], [G], [M], [V], step=0), lambda: ops.adamw_step([P.float()], [G], [M], [V], master=[V]),
-                lambda: ops.adamw_step([P], [G], [M], [V], factors=M[:3])):
+                lambda: ops.adamw_step([P], [G], [M], [V], factors=M[:3]), lambda: ops.adamw_step([P, P], [G, G], [M, V], [V, M])):
         with pytest.raises((ValueError, TypeError, RuntimeError)):
             bad()
     torch.cuda.synchronize()
     assert torch.equal(P.cpu(), p) and not M.any() and not V.any()
+
+
+def test_offsets_past_32_bits(ops):
+    """One tensor of more than 2^31 elements, 8-bit states: its end steps like a small tensor."""
+    n, last = 2 ** 31 + 256 * 40 + 77, 256 * 20 + 77
+    P = torch.full((n,), 0.5, dtype=BF16, device="cuda")
+    G = torch.full((n,), 1e-3, dtype=BF16, device="cuda")
+    (g,) = _tensors([last], BF16, BF16, 15)[1]
+    G[-last:] = g.cuda()
+    S = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = tuple([torch.zeros(-(-n // 256), device="cuda")] for _ in range(2))
+    ops.adamw_step([P], [G], [S[0]], [S[1]], step=1, scales=sc)
+    torch.cuda.synchronize()
+    p = torch.full((last,), 0.5, dtype=BF16)
+    new, m, v, root = plain_step(p, g, torch.zeros(last), torch.zeros(last), 1)
+    assert torch.equal(P[-last:].cpu(), new.to(BF16))
+    for codes, scales, (wc, ws) in ((S[0], sc[0][0], encode(m, False)), (S[1], sc[1][0], encode(root, True))):
+        assert torch.equal(codes[-last:].cpu(), wc) and torch.equal(scales[-(-(-last // 256)):].cpu(), ws)

@@ -325,3 +325,56 @@ def test_refusals(ops):
                 lambda: ops.adapter_backward(d["dY"], X, A, B, d["H"], d["dX"].float(), index), lambda: ops.adapter_plan(index, 0)):
         with pytest.raises((ValueError, TypeError, RuntimeError)):
             bad()
+
+
+@pytest.mark.parametrize("M,K,N,R,n", [(300, 256, 264, 12, 3), (140, 264, 256, 64, 2), (300, 77, 91, 5, 3)])
+def test_each_gradient_alone(ops, M, K, N, R, n):
+    """Ranks that are padded, widened or neither, on both paths: a gradient does not depend on which others are asked for."""
+    d, index = _inputs(M, K, N, R, n, BF16, 31), _index("random", M, n, 32)
+    full = check_backward(ops, d, index)
+    for need in ((True, False, False), (False, True, False), (False, False, True), (True, True, False), (False, True, True)):
+        got = ops.adapter_backward(d["dY"], d["X"], d["A"], d["B"], d["H"], d["dX"], index, d["scale"], need=need)
+        for g, w, asked in zip(got, full, need):
+            assert torch.equal(g, w) if asked else g is None
+
+
+@pytest.mark.parametrize("t", [BF16, F32])
+def test_many_rows(ops, t):
+    """More rows than the plan keeps in registers, adapters that share runs of tiles and one that has many runs."""
+    M, n = 40000, 6
+    d = _inputs(M, 64, 72, 8, n, t, 41)
+    index = _index("random", M, n, 42)
+    index[:30000] = 4
+    check_forward(ops, d, index)
+    check_backward(ops, d, index)
+
+
+def test_offsets_past_32_bits(ops):
+    """Y of more than 2^31 elements: the last rows, in the forward and the backward pass."""
+    M, K, N, R, n = 263000, 256, 8192, 8, 2
+    assert M * N > 2 ** 31
+    X = torch.randn(M, K, dtype=BF16, device="cuda")
+    Y = torch.randn(M, N, dtype=BF16, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    A = (torch.randn(n, R, K, generator=g) * K ** -0.5).to(BF16).cuda()
+    B = (torch.randn(n, N, R, generator=g) * 0.05).to(BF16).cuda()
+    index = (torch.arange(M, device="cuda") % 3 - 1).to(torch.int32)
+    rows = torch.tensor([0, 1, 2, M // 2, M - 3, M - 2, M - 1], device="cuda")
+    out, H = ops.adapter_forward(X, A, B, Y, index, keep=True)
+    dX, dA, dB = ops.adapter_backward(Y, X, A, B, H, None, index, need=(True, False, False))
+    torch.cuda.synchronize()
+    for m in rows.tolist():
+        a = int(index[m])
+        if a < 0:
+            assert torch.equal(out[m], Y[m]) and not dX[m].any()
+            continue
+        G = Y[m].double() @ B[a].double()
+        wantx = G @ A[a].double()
+        eG = p(N) * (Y[m].double().abs() @ B[a].double().abs())
+        tol = _half(BF16) * wantx.abs() + eG @ A[a].double().abs() + (p(R) + 2.0 ** -17) * (G.abs() @ A[a].double().abs())
+        _close(dX[m], wantx, tol, f"dX[{m}]")
+        h = X[m].double() @ A[a].T.double()
+        wanto = Y[m].double() + B[a].double() @ h
+        eH = p(K) * (X[m].double().abs() @ A[a].T.double().abs())
+        tolo = _half(BF16) * wanto.abs() + B[a].double().abs() @ eH + (p(R) + 2.0 ** -17) * (B[a].double().abs() @ h.abs()) + 2 * U * wanto.abs()
+        _close(out[m], wanto, tolo, f"out[{m}]")

@@ -225,3 +225,20 @@ def test_refusals(ops):
             bad()
     with pytest.raises(RuntimeError):
         ops.layernorm_forward(x, eps=-1.0)
+
+
+def test_offsets_past_32_bits(ops):
+    """More than 2^31 elements: the last rows of both passes."""
+    M, K = 1_680_000, 1288
+    assert M * K > 2 ** 31
+    x = torch.randn(M, K, dtype=BF16, device="cuda")
+    rows = torch.tensor([0, M // 2, M - 2, M - 1], device="cuda")
+    Y, mean, rstd = ops.layernorm_forward(x)
+    dX, _, db = ops.layernorm_backward(x, x, mean, rstd)
+    few = x[rows]
+    fewY, m, r = ops.layernorm_forward(few)
+    assert torch.equal(Y[rows], fewY) and torch.equal(mean[rows], m) and torch.equal(rstd[rows], r)
+    assert torch.equal(dX[rows], ops.layernorm_backward(few, few, m, r)[0])
+    # column sums over 1.68 M rows: a thread adds M / (148 * 3) of them, ten times the rows of the bound above
+    want, size = x.sum(0, dtype=torch.float64), x.abs().sum(0, dtype=torch.float64)
+    _close(db, want, _half(BF16) * want.abs() + (M / 444 + 32) * U * size, "dbias")
