@@ -436,7 +436,11 @@ SS1_API int ss1_test_bounds_check(int64_t index, int64_t extent);
  * or an output. All can be captured into a CUDA graph. Matrices are dense row-major; pointers need
  * the alignment of their element only (rows and bases on 16-byte boundaries take the faster
  * kernels). Sums, statistics and products are float32. Outputs must not overlap inputs unless
- * stated. A NaN or an infinity stays within the outputs that its formula reaches.
+ * stated. What is not finite stays within the outputs that its formula reaches, and may be NaN
+ * there where the formula has an infinity. The kernels are launched with programmatic dependent
+ * launch: they may start while the previous kernel on the stream is running, but read and write
+ * nothing before it is over, so stream order holds as for any launch. Tensor-core kernels bound their
+ * waits (2 s); one that ran out would leave NaN in what it computes.
  */
 
 /*
@@ -464,10 +468,10 @@ SS1_API int ss1_layernorm_backward_workspace(int64_t M, int64_t K, size_t* bytes
  *   weight : device, [K] of `w_dtype`, or NULL (1).
  *   dX     : device, [M, K] of `dtype`, written, or NULL (not computed).
  *   dweight, dbias : device, [K] of `w_dtype`, overwritten (zero when M == 0), or NULL.
- *   workspace : device, 16-byte aligned, at least ss1_layernorm_backward_workspace bytes; not
- *            needed where dweight and dbias are NULL. Calls that share one must be ordered.
+ *   workspace : device, 16-byte aligned, at least ss1_layernorm_backward_workspace bytes (0 for few
+ *            elements); not needed where dweight and dbias are NULL. Calls that share one must be ordered.
  * The column sums are added in a fixed order: repeated calls give the same bits. Asynchronous.
- * Errors: as ss1_layernorm_forward; INVALID_ARG for a workspace that is too small.
+ * A row whose statistics are not finite leaves NaN in all of dweight. Errors: as ss1_layernorm_forward; INVALID_ARG for a workspace that is too small.
  */
 SS1_API int ss1_layernorm_backward(const void* dY, const void* X, const float* mean, const float* rstd, const void* weight,
                                    void* dX, void* dweight, void* dbias, int64_t M, int64_t K, int dtype, int w_dtype,
@@ -547,7 +551,8 @@ SS1_API int ss1_adapter_backward(const ss1_adapters* adapters, const void* dY, c
  * elements (the last one of a tensor may be shorter) share one float scale, the smallest power of
  * two from 2^-126 on that brings the block's largest magnitude to 448 or below; held are OCP FP8
  * E4M3 codes of m / scale and of sqrt(v) / scale (rounded to nearest even, a positive root at least
- * to the smallest code). The step uses the new moments before they are rounded.
+ * to the smallest code; a NaN is held as NaN and does not count for the scale, an infinity makes it
+ * 2^120). The step uses the new moments before they are rounded.
  */
 #define SS1_ADAMW_BLOCK 256
 #define SS1_ADAMW_FACTORS 9

@@ -229,7 +229,6 @@ template <int N, int BITS>
 __global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
                                                             const float* __restrict__ device, float minus_zero) {
     wait_for_previous();
-    let_next_start();
     const F2 none = F2::both(minus_zero);
     Factors f = host;
     if (device) {

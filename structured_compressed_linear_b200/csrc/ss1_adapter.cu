@@ -452,12 +452,13 @@ __global__ void __launch_bounds__(256) tile_update_kernel(const float* __restric
 }
 
 // D_a[c, r] = f * sum over adapter a's rows of U[m, c] P[m, r], for one share of the rows (blockIdx.z):
-// element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs. A thread is a column; 32 rows' P
+// element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs of D, or of `out` where there is one share. A
+// thread is a column; 32 rows' P
 // lie in shared memory, and 32 rows of U are on their way at a time.
 template <typename T>
 __global__ void __launch_bounds__(128) column_sums_kernel(const T* __restrict__ U, const float* __restrict__ P, PlanView plan,
-                                                          const float* __restrict__ scale, float* __restrict__ D, int64_t M,
-                                                          int C, int R, int n, int cs, int rs, int site_u) {
+                                                          const float* __restrict__ scale, float* __restrict__ D, T* __restrict__ out,
+                                                          int64_t M, int C, int R, int n, int cs, int rs, int site_u) {
     __shared__ __align__(16) float p[kSub][kRanks];
     __shared__ int64_t rows[kSub];
     const int a = blockIdx.y % n, r0 = (blockIdx.y / n) * kRanks, ranks = min(kRanks, R - r0);
@@ -502,7 +503,10 @@ __global__ void __launch_bounds__(128) column_sums_kernel(const T* __restrict__ 
     const int64_t base = (int64_t)blockIdx.z * size + (int64_t)a * C * R + (int64_t)c * cs;
 #pragma unroll
     for (int r = 0; r < kRanks; ++r)
-        if (r < ranks && SS1_IN(base + (int64_t)(r0 + r) * rs, size * shares, kSiteAdaPart)) D[base + (int64_t)(r0 + r) * rs] = f * s[r];
+        if (r < ranks && SS1_IN(base + (int64_t)(r0 + r) * rs, size * shares, kSiteAdaPart)) {
+            if (shares == 1) out[base + (int64_t)(r0 + r) * rs] = from_f<T>(f * s[r]);
+            else D[base + (int64_t)(r0 + r) * rs] = f * s[r];
+        }
 }
 
 // out[i] = the shares' partial sums, added in share order.
@@ -584,9 +588,10 @@ cudaError_t column_sums(const Call& c, const void* U, const float* P, const floa
                         int rs, int site, cudaStream_t st) {
     const int shares = general_shares(c.M, C, c.R, c.n);
     const dim3 grid((unsigned)((C + 127) / 128), (unsigned)(c.n * ((c.R + kRanks - 1) / kRanks)), (unsigned)shares);
-    column_sums_kernel<T><<<grid, 128, 0, st>>>((const T*)U, P, c.plan, scale, part, c.M, (int)C, c.R, c.n, cs, rs, site);
+    column_sums_kernel<T><<<grid, 128, 0, st>>>((const T*)U, P, c.plan, scale, part, (T*)D, c.M, (int)C, c.R, c.n, cs, rs, site);
     const int64_t size = (int64_t)c.n * C * c.R;
-    add_shares_kernel<T><<<(unsigned)((size + 255) / 256), 256, 0, st>>>(part, (T*)D, size, shares);
+    if (shares > 1)      // one share writes D itself
+        add_shares_kernel<T><<<(unsigned)((size + 255) / 256), 256, 0, st>>>(part, (T*)D, size, shares);
     return cudaGetLastError();
 }
 

@@ -144,7 +144,9 @@ inline bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr
 // (programmatic dependent launch). Rules that every kernel launched like this keeps: all its CTAs execute
 // griddepcontrol.wait before they end, so that what it has waited for is over for whoever waits for it; and
 // before the wait it touches nothing that an earlier kernel may still write. A kernel lets its
-// successor start only after its own wait, except where its successor waits first thing.
+// successor start only after its own wait, except where its successor waits first thing; and only where the
+// successor has something to do before its wait, because CTAs that merely wait settle unevenly on the
+// SMs (layer norm forward 4096 x 4096: 17.4 us with, 15.4 without).
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};

@@ -38,12 +38,12 @@ def test_layernorm_forward(lib):
 
 def test_layernorm_backward(lib):
     n = ctypes.c_size_t()
-    assert lib.ss1_layernorm_backward_workspace(100, 64, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.ss1_layernorm_backward_workspace(4000, 64, ctypes.byref(n)) == 0 and n.value > 0
     assert lib.ss1_layernorm_backward_workspace(-1, 64, ctypes.byref(n)) == -1
     assert lib.ss1_layernorm_backward_workspace(1, 0, ctypes.byref(n)) == -1
     assert lib.ss1_layernorm_backward_workspace(1, 1, None) == -1
-    lib.ss1_layernorm_backward_workspace(4, 8, ctypes.byref(n))
-    ok = dict(dY=P, X=P, mean=P, rstd=P, w=P, dX=P, dw=P, db=P, M=4, K=8, dtype=0, wt=0, ws=P, size=n.value, st=None)
+    lib.ss1_layernorm_backward_workspace(4000, 64, ctypes.byref(n))
+    ok = dict(dY=P, X=P, mean=P, rstd=P, w=P, dX=P, dw=P, db=P, M=4000, K=64, dtype=0, wt=0, ws=P, size=n.value, st=None)
 
     def call(**change):
         return lib.ss1_layernorm_backward(*dict(ok, **change).values())
