@@ -13,8 +13,6 @@
 #include "ss1_ops.cuh"
 #include "ptx_sm100.cuh"
 
-#include <string.h>
-
 namespace ss1 {
 namespace {
 
@@ -22,19 +20,28 @@ using namespace op;
 
 constexpr int kUnit = 8;   // elements a thread takes at a time: 16 bytes of bf16, 32 of float
 
-// Eight elements of a row. Vector form: consecutive, from 8 * (unit * width + t); scalar form (rows
-// that do not start on 16-byte boundaries): strided by the width, so that a warp's loads stay
-// together. They are worked on as four pairs.
-template <bool VEC>
+// Eight elements of a row, a thread's unit. kRow8: consecutive (bf16 rows on 16-byte boundaries); kRow44: twice four
+// consecutive ones, half the unit's columns apart, so that a warp's 16-byte pieces of float rows lie side by
+// side; kRow1: strided by the width (rows that do not start on 16-byte boundaries), so that its elements do. They
+// are worked on as four pairs.
+enum Form { kRow1, kRow8, kRow44 };
+template <typename T, bool VEC>
+constexpr Form form_of() { return !VEC ? kRow1 : (sizeof(T) == 4 ? kRow44 : kRow8); }
+
+template <Form F>
 __device__ __forceinline__ int unit_first(int unit, int width, int t) {
-    return VEC ? (unit * width + t) * kUnit : unit * width * kUnit + t;
+    return F == kRow8 ? (unit * width + t) * kUnit : unit * width * kUnit + (F == kRow44 ? t * 4 : t);
+}
+template <Form F>
+__device__ __forceinline__ int unit_at(int first, int width, int i) {      // column of the unit's element i
+    return F == kRow8 ? first + i : (F == kRow44 ? first + (i < 4 ? i : width * 4 + i - 4) : first + i * width);
 }
 
 // `p` is the row (or the weights), `left` what `total` leaves behind it; elements past K are `other`.
-template <typename T, bool VEC>
+template <typename T, Form F>
 __device__ __forceinline__ void load_unit(const T* __restrict__ p, [[maybe_unused]] int64_t left, int first, int width, int K, F2 (&f)[4],
                                           float other, int site) {
-    if (VEC) {
+    if constexpr (F == kRow8) {
         if (first < K && SS1_SPAN_IN(first, kUnit, left, site)) {
             Raw8<T> r;
             r.load(p + first);
@@ -43,11 +50,20 @@ __device__ __forceinline__ void load_unit(const T* __restrict__ p, [[maybe_unuse
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = F2::both(other);
         }
+    } else if constexpr (F == kRow44) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = unit_at<F>(first, width, 4 * h);
+            float4 v = make_float4(other, other, other, other);
+            if (k < K && SS1_SPAN_IN(k, 4, left, site)) v = *reinterpret_cast<const float4*>(p + k);
+            f[2 * h] = F2::of(v.x, v.y);
+            f[2 * h + 1] = F2::of(v.z, v.w);
+        }
     } else {
         float v[kUnit];
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-            const int k = first + i * width;
+            const int k = unit_at<F>(first, width, i);
             v[i] = k < K && SS1_IN(k, left, site) ? to_f(p[k]) : other;
         }
 #pragma unroll
@@ -55,17 +71,24 @@ __device__ __forceinline__ void load_unit(const T* __restrict__ p, [[maybe_unuse
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, Form F>
 __device__ __forceinline__ void store_unit(T* __restrict__ p, [[maybe_unused]] int64_t left, int first, int width, int K,
                                            const F2 (&f)[4], int site) {
-    if (VEC) {
+    if constexpr (F == kRow8) {
         Raw8<T> r;
         r.set(f);
         if (first < K && SS1_SPAN_IN(first, kUnit, left, site)) r.store(p + first);
+    } else if constexpr (F == kRow44) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = unit_at<F>(first, width, 4 * h);
+            if (k < K && SS1_SPAN_IN(k, 4, left, site))
+                *reinterpret_cast<float4*>(p + k) = make_float4(f[2 * h].lo(), f[2 * h].hi(), f[2 * h + 1].lo(), f[2 * h + 1].hi());
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-            const int k = first + i * width;
+            const int k = unit_at<F>(first, width, i);
             if (k < K && SS1_IN(k, left, site)) p[k] = from_f<T>(i % 2 ? f[i / 2].hi() : f[i / 2].lo());
         }
     }
@@ -83,21 +106,22 @@ constexpr bool in_ring() { return VEC || sizeof(T) == 4; }
 
 // `first` as unit_first gives it, from the start of the row at `p`; nothing is read where the row is not `ok`, or behind
 // its end (zeros instead). FULL: every unit lies inside the row.
-template <typename T, bool VEC, bool FULL>
+template <typename T, Form F, bool FULL>
 __device__ __forceinline__ void unit_ahead(uint32_t ring, int threads, const T* p, [[maybe_unused]] int64_t left, int first, int width, int K,
                                            bool ok, const T* any, int site) {
-    if (VEC) {
-        const bool in = ok && (FULL || first < K) && SS1_SPAN_IN(first, kUnit, left, site);
-        const T* from = in ? p + first : any;
+    if constexpr (F != kRow1) {
 #pragma unroll
-        for (int i = 0; i < unit_bytes<T>() / 16; ++i)
+        for (int i = 0; i < unit_bytes<T>() / 16; ++i) {
+            const int k = unit_at<F>(first, width, i * (16 / (int)sizeof(T)));
+            const bool in = ok && (FULL || k < K) && SS1_SPAN_IN(k, 16 / (int)sizeof(T), left, site);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + (i * threads + threadIdx.x) * 16),
-                         "l"(from + i * (16 / sizeof(T))), "r"(in ? 16 : 0)
+                         "l"(in ? p + k : any), "r"(in ? 16 : 0)
                          : "memory");
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-            const int k = first + i * width;
+            const int k = unit_at<F>(first, width, i);
             const bool in = ok && k < K && SS1_IN(k, left, site);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + (i * threads + threadIdx.x) * 4),
                          "l"(in ? p + k : any), "r"(in ? 4 : 0)
@@ -106,15 +130,19 @@ __device__ __forceinline__ void unit_ahead(uint32_t ring, int threads, const T* 
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, Form F>
 __device__ __forceinline__ void unit_back(const uint8_t* ring, int threads, F2 (&f)[4]) {
-    if (VEC) {
-        uint4 v[unit_bytes<T>() / 16];
-#pragma unroll
-        for (int i = 0; i < unit_bytes<T>() / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(ring + (i * threads + threadIdx.x) * 16);
+    if constexpr (F == kRow8) {
         Raw8<T> r;
-        memcpy(&r, v, sizeof r);
+        r.a = *reinterpret_cast<const uint4*>(ring + threadIdx.x * 16);
         r.get(f);
+    } else if constexpr (F == kRow44) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 v = *reinterpret_cast<const float4*>(ring + (h * threads + threadIdx.x) * 16);
+            f[2 * h] = F2::of(v.x, v.y);
+            f[2 * h + 1] = F2::of(v.z, v.w);
+        }
     } else {
         const float* v = reinterpret_cast<const float*>(ring) + threadIdx.x;
 #pragma unroll
@@ -143,10 +171,10 @@ __device__ __forceinline__ float row_sum(float v, int width, float* buf) {
 
 // CTAs meant to be on an SM: about 768 threads of up to 85 registers; rows of more than 256 threads 1024 of 64
 constexpr int fwd_ctas(int threads) { return threads <= 256 ? 768 / threads : 1024 / threads; }
-// Rows ahead: what keeps about 128 KB in flight on an SM, one to three.
+// Rows ahead: what keeps about 64 KB in flight on an SM beside the rows being read, one to three (128 KB: 5 % slower).
 template <typename T>
 constexpr int fwd_ahead(int units, int threads) {
-    const int rows = 131072 / (fwd_ctas(threads) * units * unit_bytes<T>() * threads);
+    const int rows = 65536 / (fwd_ctas(threads) * units * unit_bytes<T>() * threads);
     return rows > 3 ? 3 : (rows < 1 ? 1 : rows);
 }
 
@@ -164,6 +192,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
     __shared__ __align__(16) float buf[2][32];
     wait_for_previous();
 
+    constexpr Form F = form_of<T, VEC>();
     constexpr bool kRing = in_ring<T, VEC>(), kShared = WARP && VEC;
     constexpr int kDepth = fwd_ahead<T>(NU, THREADS), kPlace = unit_bytes<T>() * THREADS, kRow = NU * kPlace;
     __shared__ __align__(16) float weights[kShared ? 2 : 1][kShared ? NU * 2 : 1][kShared ? 128 : 4];   // [w, b][half unit][lane * 4]
@@ -180,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
         if (from_row < M) {
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                unit_ahead<T, VEC, FULL>(place + slot * kRow + u * kPlace, THREADS, from, (M - from_row) * K, unit_first<VEC>(u, width, t),
+                unit_ahead<T, F, FULL>(place + slot * kRow + u * kPlace, THREADS, from, (M - from_row) * K, unit_first<F>(u, width, t),
                                          width, K, true, X, kSiteNormX);
         }
         from += stride;
@@ -191,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
     for (int i = 0; i < kDepth; ++i) ahead(i);
     if (kShared) {
         for (int i = threadIdx.x; i < NU * 256; i += THREADS) {      // element i of the row: unit, lane, half, place in the half
-            const int u = i / 256, l = i / 8 % 32, h = i / 4 % 2;
+            const int u = i / 256, l = F == kRow44 ? i / 4 % 32 : i / 8 % 32, h = F == kRow44 ? i / 128 % 2 : i / 4 % 2;
             weights[0][u * 2 + h][l * 4 + i % 4] = w && i < K ? to_f(w[i]) : 1.0f;
             weights[kShared][u * 2 + h][l * 4 + i % 4] = b && i < K ? to_f(b[i]) : 0.0f;
         }
@@ -210,9 +239,9 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             if (kRing) {
-                unit_back<T, VEC>(ring + slot * kRow + u * kPlace, THREADS, x[u]);
+                unit_back<T, F>(ring + slot * kRow + u * kPlace, THREADS, x[u]);
             } else {
-                load_unit<T, VEC>(in, left, unit_first<VEC>(u, width, t), width, K, x[u], 0.0f, kSiteNormX);
+                load_unit<T, F>(in, left, unit_first<F>(u, width, t), width, K, x[u], 0.0f, kSiteNormX);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) s = s + x[u][i];
@@ -223,18 +252,14 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
         F2 q = F2::both(0.0f);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const int first = unit_first<VEC>(u, width, t);
+            const int first = unit_first<F>(u, width, t);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + less;
-            if (VEC) {
-                if (!FULL && first >= K) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[u][i] = F2::both(0.0f);
-                }
-            } else {
+            if (!FULL) {          // what lies behind the row's end deviates by nothing
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    x[u][i] = F2::of(first + 2 * i * width < K ? x[u][i].lo() : 0.0f, first + (2 * i + 1) * width < K ? x[u][i].hi() : 0.0f);
+                    x[u][i] = F2::of(unit_at<F>(first, width, 2 * i) < K ? x[u][i].lo() : 0.0f,
+                                     unit_at<F>(first, width, 2 * i + 1) < K ? x[u][i].hi() : 0.0f);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
@@ -243,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
         const F2 by = F2::both(rstd);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const int first = unit_first<VEC>(u, width, t);
+            const int first = unit_first<F>(u, width, t);
             F2 wv[4], bv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] * by;
@@ -256,9 +281,9 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
                     x[u][2 * h + 1] = fma2(x[u][2 * h + 1], F2::of(wh.z, wh.w), F2::of(bh.z, bh.w));
                 }
             } else if (w) {
-                load_unit<W, VEC>(w, K, first, width, K, wv, 1.0f, kSiteNormW);
+                load_unit<W, F>(w, K, first, width, K, wv, 1.0f, kSiteNormW);
                 if (b) {
-                    load_unit<W, VEC>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
+                    load_unit<W, F>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[u][i] = fma2(x[u][i], wv[i], bv[i]);
                 } else {
@@ -266,11 +291,11 @@ __global__ void __launch_bounds__(THREADS, fwd_ctas(THREADS)) norm_fwd_kernel(co
                     for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] * wv[i];
                 }
             } else if (b) {
-                load_unit<W, VEC>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
+                load_unit<W, F>(b, K, first, width, K, bv, 0.0f, kSiteNormW);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] + bv[i];
             }
-            store_unit<T, VEC>(out, left, first, width, FULL ? 1 << 30 : K, x[u], kSiteNormY);
+            store_unit<T, F>(out, left, first, width, FULL ? 1 << 30 : K, x[u], kSiteNormY);
         }
         if (t == 0) {
             if (mean_out) mean_out[row] = mean;
@@ -403,6 +428,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
     static_assert(UNITS * ROWS == 2, "one turn's pieces");
     extern __shared__ __align__(16) uint8_t ring[];             // the turns ahead, later [groups][2][K] sums
     __shared__ __align__(16) float4 buf[2][15][16];             // a row's two sums of each warp, for two rows
+    constexpr Form F = form_of<T, VEC>();
     constexpr bool kRing = in_ring<T, VEC>();
     constexpr int kDepth = bwd_ahead<T>(), kPlace = unit_bytes<T>() * kBwdThreads, kTurn = 4 * kPlace;
     wait_for_previous();
@@ -417,7 +443,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
     for (int u = 0; u < UNITS; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) { sw[u][i] = sb[u][i] = F2::both(0.0f); wv[u][i] = F2::both(1.0f); }
-        if (w) load_unit<W, VEC>(w, K, unit_first<VEC>(u, width, t), width, K, wv[u], 0.0f, kSiteNormW);
+        if (w) load_unit<W, F>(w, K, unit_first<F>(u, width, t), width, K, wv[u], 0.0f, kSiteNormW);
     }
     int64_t row = ((int64_t)blockIdx.x * groups + g) * ROWS, from = row;
     const uint32_t place = ptx::smem_u32(ring);
@@ -427,10 +453,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
 #pragma unroll
             for (int e = 0; e < 2; ++e) {                       // the turn's two units: two rows', or one row's
                 const int64_t r = from + (ROWS == 2 ? e : 0), at = r * K;
-                const int first = unit_first<VEC>(ROWS == 2 ? 0 : e, width, t);
-                unit_ahead<T, VEC, false>(place + slot * kTurn + e * 2 * kPlace, kBwdThreads, X + at, total - at, first, width, K, r < M, X,
+                const int first = unit_first<F>(ROWS == 2 ? 0 : e, width, t);
+                unit_ahead<T, F, false>(place + slot * kTurn + e * 2 * kPlace, kBwdThreads, X + at, total - at, first, width, K, r < M, X,
                                           kSiteNormX);
-                unit_ahead<T, VEC, false>(place + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dY + at, total - at, first, width, K,
+                unit_ahead<T, F, false>(place + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dY + at, total - at, first, width, K,
                                           r < M, dY, kSiteNormX);
             }
         }
@@ -454,14 +480,14 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (kRing) {
-                unit_back<T, VEC>(ring + slot * kTurn + e * 2 * kPlace, kBwdThreads, x[e]);
-                unit_back<T, VEC>(ring + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dy[e]);
+                unit_back<T, F>(ring + slot * kTurn + e * 2 * kPlace, kBwdThreads, x[e]);
+                unit_back<T, F>(ring + slot * kTurn + (e * 2 + 1) * kPlace, kBwdThreads, dy[e]);
             } else {
                 const int64_t r = row + (ROWS == 2 ? e : 0);
                 const int k = r < M ? K : 0;
-                const int first = unit_first<VEC>(ROWS == 2 ? 0 : e, width, t);
-                load_unit<T, VEC>(X + r * K, total - r * K, first, width, k, x[e], 0.0f, kSiteNormX);
-                load_unit<T, VEC>(dY + r * K, total - r * K, first, width, k, dy[e], 0.0f, kSiteNormX);
+                const int first = unit_first<F>(ROWS == 2 ? 0 : e, width, t);
+                load_unit<T, F>(X + r * K, total - r * K, first, width, k, x[e], 0.0f, kSiteNormX);
+                load_unit<T, F>(dY + r * K, total - r * K, first, width, k, dy[e], 0.0f, kSiteNormX);
             }
         }
         ahead(slot);
@@ -518,7 +544,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[e][i] = (fma2(x[e][i], mb, dy[e][i]) + ma) * by;
             if (row + r < M)
-                store_unit<T, VEC>(dX + (row + r) * K, total - (row + r) * K, unit_first<VEC>(ROWS == 2 ? 0 : e, width, t), width, K, x[e],
+                store_unit<T, F>(dX + (row + r) * K, total - (row + r) * K, unit_first<F>(ROWS == 2 ? 0 : e, width, t), width, K, x[e],
                                    kSiteNormY);
         }
     }
@@ -533,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const T* __restri
     for (int u = 0; u < UNITS; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-            const int first = unit_first<VEC>(u, width, t), k = VEC ? first + i : first + i * width;
+            const int k = unit_at<F>(unit_first<F>(u, width, t), width, i);
             if (k < K) {
                 col[k] = i % 2 ? sw[u][i / 2].hi() : sw[u][i / 2].lo();
                 col[K + k] = i % 2 ? sb[u][i / 2].hi() : sb[u][i / 2].lo();
