@@ -146,6 +146,22 @@ def test_nan_and_infinity_stay_in_their_row(ops):
     assert torch.equal(Y[rows], clean[rows]) and Y[7].isnan().all() and Y[21].isnan().any()
 
 
+@pytest.mark.parametrize("K", [1, 4, 8, 512])
+def test_mean_that_overflows_behind_the_rows_end(ops, K):
+    """(0 - mean) rstd is past float32 here, and nothing behind the row's end may come of it. K is a power of two, so
+    that mean is x, xhat 0 and dX = rstd (dy - mean(dy)): the sum over K is the one rounding that counts."""
+    x = torch.full((3, K), 2.0 ** 66, device="cuda")
+    dy = torch.randn(3, K, generator=torch.Generator().manual_seed(K)).cuda()
+    Y, mean, rstd = ops.layernorm_forward(x, eps=2.0 ** -124)
+    assert bool((Y == 0).all()) and bool((mean == 2.0 ** 66).all()) and bool(((rstd / 2.0 ** 62 - 1).abs() <= 4 * U).all())
+    dX, dw, db = ops.layernorm_backward(dy, x, mean, rstd)
+    d = dy.double()
+    scale = rstd.double()[:, None]
+    _close(dX, scale * (d - d.mean(1, keepdim=True)), N * U * scale * (d.abs() + d.abs().mean(1, keepdim=True)), "dX")
+    assert bool((dw == 0).all())
+    _close(db, d.sum(0), N * U * d.abs().sum(0), "db")
+
+
 @pytest.mark.parametrize("K", [1280, 1021])
 def test_outputs_end_where_they_end(ops, K):
     """Unaligned bases (the scalar kernels) and guard elements around the outputs, through the C entry points."""
