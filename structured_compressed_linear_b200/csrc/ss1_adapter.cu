@@ -665,6 +665,7 @@ Call call_of(const ss1_adapters& ad, int64_t M) {
     c.A = ad.A; c.B = ad.B; c.scale = ad.scale; c.index = ad.index;
     c.M = M; c.K = ad.K; c.N = ad.N; c.R = ad.R; c.n = ad.count;
     c.plan = PlanView{};
+    c.planned = false;
     return c;
 }
 
@@ -672,6 +673,7 @@ Call call_of(const ss1_adapters& ad, int64_t M) {
 cudaError_t plan_of(const ss1_adapters& ad, int64_t M, void* ws, Call& c, cudaStream_t st) {
     if (!ad.index) return cudaSuccess;
     c.plan = plan_view(ad.plan ? const_cast<void*>(ad.plan) : ws, M, ad.count);
+    c.planned = ad.plan == nullptr;
     return ad.plan ? cudaSuccess : launch_plan(ad.index, M, ad.count, c.plan, st);
 }
 

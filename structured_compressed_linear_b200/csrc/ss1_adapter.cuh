@@ -34,6 +34,7 @@ struct Call {
     PlanView plan;
     int64_t M, K, N;
     int R, n;
+    bool planned;            // the plan's kernel is part of this call
 };
 
 // Shares of an adapter's rows in the sums of dA and dB (general path).
