@@ -1085,9 +1085,10 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
 int mma_rank(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
 
 int mma_runs(int64_t M, int64_t C, int n) {
-    // at least two tiles a run
+    // one CTA an SM for each gradient, since both launches do other work beside (two: 8192 x 768 x 2304, rank 32, 57 us
+    // instead of 48), and a run for every tile while they are few (two tiles a run: 2048 x 768 x 2304 37 us instead of 29)
     int64_t s = kColumnsCtas / ((C + kColCols - 1) / kColCols);
-    const int64_t most = (M / kTile + 1) / 2;
+    const int64_t most = M / kTile + n;
     s = s > most ? most : s;
     return (int)(s < 1 ? 1 : s);
 }
