@@ -31,9 +31,10 @@ using namespace op;
 // adapter find one another by a ballot for each bit of its number: one __match_any_sync takes a step for every
 // different value, 18 us for 8192 rows of 32 adapters in random order), the counts are scanned over
 // adapters and warps, and each row's place is what comes before it: rows keep their order within an
-// adapter. The first kAhead index words of a lane are loaded together, and their places within the warp kept
-// (32 warps cover 16,384 rows that way): one memory latency, and one walk; rows beyond are walked twice.
-constexpr int kAhead = 16;
+// adapter. The first AHEAD index words of a lane are loaded together, and their places within the warp kept:
+// one memory latency, and one walk; rows beyond are walked twice. AHEAD is 8 where 32 warps (fewer beside many
+// adapters) cover all rows so, since code that is not fetched yet is what a small plan waits for: 3.2 us against 4.4
+// with 16 at 300 rows, 4.4 against 5.7 at 8192; 16 beyond: 16,384 rows 7.8 us against 10.2 with 8.
 
 __device__ __forceinline__ int plan_group(const int32_t* __restrict__ index, int row, int end, int n) {
     if (row >= end) return -1;
@@ -41,6 +42,7 @@ __device__ __forceinline__ int plan_group(const int32_t* __restrict__ index, int
     return (unsigned)a < (unsigned)n ? a : n;
 }
 
+template <int AHEAD>
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ index, int M, int n, PlanView plan) {
     extern __shared__ int cnt[];   // [warps][n + 1], then [n + 2] first rows and [n + 2] first tiles
     wait_for_previous();
@@ -51,9 +53,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     int* first_tile = first + n + 2;
     const int share = (M + warps - 1) / warps;
     const int begin = min(M, warp * share), end = min(M, begin + share);
-    int ahead[kAhead];
+    int ahead[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) ahead[i] = plan_group(index, begin + i * 32 + lane, end, n);
+    for (int i = 0; i < AHEAD; ++i) ahead[i] = plan_group(index, begin + i * 32 + lane, end, n);
     for (int i = threadIdx.x; i < warps * groups; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
     int* mine = cnt + warp * groups;
@@ -78,10 +80,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
         __syncwarp();
         return before;
     };
-    int nth[kAhead];
+    int nth[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) nth[i] = begin + i * 32 < end ? count(ahead[i]) : 0;
-    for (int at = begin + kAhead * 32; at < end; at += 32) count(plan_group(index, at + lane, end, n));
+    for (int i = 0; i < AHEAD; ++i) nth[i] = begin + i * 32 < end ? count(ahead[i]) : 0;
+    for (int at = begin + AHEAD * 32; at < end; at += 32) count(plan_group(index, at + lane, end, n));
     __syncthreads();
     // totals, then their exclusive sums (one warp, 32 groups at a time), with the tiles' beside them
     for (int a = warp; a < groups; a += warps) {       // a warp a group, a lane a warp's count
@@ -145,14 +147,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
         if (SS1_IN(to, M, kSitePlan)) plan.rows[to] = row;
     };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < AHEAD; ++i)
         if (ahead[i] >= 0) put(ahead[i], begin + i * 32 + lane, so_far[ahead[i]] + nth[i]);
-    if (begin + kAhead * 32 >= end) return;    // the whole warp
+    if (begin + AHEAD * 32 >= end) return;    // the whole warp
     __syncwarp();
-    // the second walk counts on from the first kAhead rounds
+    // the second walk counts on from the first AHEAD rounds
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) count(ahead[i]);
-    for (int at = begin + kAhead * 32; at < end; at += 32) {
+    for (int i = 0; i < AHEAD; ++i) count(ahead[i]);
+    for (int at = begin + AHEAD * 32; at < end; at += 32) {
         const int a = plan_group(index, at + lane, end, n);
         const int number = count(a);
         if (a >= 0) put(a, at + lane, number);
@@ -164,7 +166,7 @@ cudaError_t launch_plan(const int32_t* index, int64_t M, int n, PlanView plan, c
     int warps = (48 * 1024 / 4 - 2 * (n + 2)) / (n + 1);
     warps = warps > 32 ? 32 : warps;
     const size_t smem = ((size_t)warps * (n + 1) + 2 * (n + 2)) * sizeof(int);
-    return launch_dependent(&plan_kernel, dim3(1), dim3((unsigned)(warps * 32)), smem, st, index, (int)M, n, plan);
+    return launch_dependent(M <= (int64_t)warps * 32 * 8 ? &plan_kernel<8> : &plan_kernel<16>, dim3(1), dim3((unsigned)(warps * 32)), smem, st, index, (int)M, n, plan);
 }
 
 namespace {
