@@ -15,6 +15,10 @@
 // Memory-bound: bf16 weights with a float32 master copy move 28 bytes an element with float32
 // moments, 16 with 8-bit ones. Every float32 operation is rounded on its own (no fused multiply-
 // add), so that the codes are those of the same formula written with elementwise operations.
+//
+// 30 M bf16 weights with master copies: float32 moments 134 us (840 MB at 6.3 TB/s, 0.96 of the copy rate); 8 bits 93 us
+// (482 MB, 5.2 TB/s, 0.79; 106 with three CTAs an SM), where the issue slots of each element's root and quotient
+// (57 % busy) and the loads that 64 registers a thread keep in flight bound it together.
 #include "ss1_ops.cuh"
 
 #include <cuda_fp16.h>

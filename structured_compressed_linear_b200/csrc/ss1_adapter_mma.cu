@@ -4,11 +4,17 @@
 //   update   : out[m, c] = in[m, c] + sum_r P[m, r] T_a[c, r]    out = Y + s H B^T,   dX + G A
 //   columns  : D_a[c, r] = sum_m U[m, c] P[m, r]             dA = G^T X,        dB = dY^T (s H)
 //
-// Each streams its [rows, columns] matrix once and does 2 R (4 R where P is split) flops for each
-// element: at ranks up to 32 that is below what mma.sync sustains beside a full HBM stream, so these
-// kernels are built as streams (cp.async rings, 16-byte vectors, rows gathered through the plan by
-// their own pointers) with register-accumulator MMAs inside, and not around tcgen05 tiles, whose
-// 128-wide accumulators an adapter's few columns would leave idle.
+// Each streams its [rows, columns] matrix once and does 2 R (4 R where P is split) flops for each element: at
+// ranks up to 32 far below what the tensor cores sustain beside a full HBM stream, so these kernels are
+// built as streams: cp.async rings, 16-byte vectors, rows gathered through the plan by their own pointers. What
+// multiplies follows from what the result needs. G, dA and dB take tcgen05 out of the ring as it lies, with the sums in
+// tensor memory: one thread issues a stage, and the other warps only load. H is handed out in float32, which tensor
+// memory's truncating sums over thousands of columns would cost digits, and `update` starts from `in` and
+// writes each element once: these two keep mma.sync and sums in registers.
+//
+// Ranks are padded to 16, 32, 64 or 128 (RT). Whole passes, us as graph replays beside what their bytes take at the measured
+// 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 59 (41.7); 16384 x 4096 x 4096: 86 (61.8). Backward, one
+// adapter of 4096 x 4096 x 4096, rank 16: 39 (20.6), rank 64: 56, rank 128: 99; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
 //
 // P between the kernels: rows in plan order, [2][RT] bf16 each: the value rounded to bf16, and
 // what that left out, rounded again (2^-17 of the value is lost). The products with both parts are
@@ -140,7 +146,8 @@ __device__ __forceinline__ void bring_ahead(const Ahead& h, int cta, int ctas) {
 // ---- prepare ---------------------------------------------------------------------------------
 
 // What the other kernels read in another form, in one launch: CTAs 0 .. nh - 1 pack the caller's H, then
-// nb widen B's rows to a multiple of 8 elements, the rest transpose A 32 x 32 at a time.
+// nb widen B's rows to a multiple of 8 elements, the rest transpose A 32 x 32 at a time (update_role reads whole
+// rows of ranks). Latency bounds it: 3.5 us at 8192 x 768, rank 32, four adapters, mostly beside the plan.
 struct Prepare {
     const float* H;            // [M, R] -> packed_h, scaled
     const int32_t* index;
@@ -218,7 +225,8 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, Plan
 // products meet in distributed shared memory and are added in CTA order. 256 threads: warp w owns rows
 // 16 w .. 16 w + 15. Stages of 64 columns: U [128][64] in 128-byte rows with the 16-byte chunks
 // XOR-swizzled by the row, and T likewise: [RT][64] (TRANS false: T_a is [R, C]) or boxes of [64][64] (TRANS true: T_a
-// is [C, ld]). H (TRANS false) is handed out in float32, so each stage's MMAs start from zero and are
+// is [C, ld]). Bound by latency, a look-up of the tile, one of its rows and nine stages a CTA: 14 us for 4096 x 4096 in
+// ragged rows (34 MB, 5.1 us at the copy rate), the plan's time hidden in part by bring_ahead. H (TRANS false) is handed out in float32, so each stage's MMAs start from zero and are
 // added in registers: the tensor core's own accumulation truncates, over thousands of columns by more than
 // float32's rounding. G (TRANS true) only feeds bf16 results: tcgen05 multiplies out of the ring as it lies
 // there and accumulates in tensor memory, one thread issuing four instructions a stage.
@@ -475,7 +483,8 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const Products d, co
 // n-tiles are eight consecutive columns: it reads 16 bytes of the box, which become the MMAs' initial
 // accumulators, and writes 16 bytes to `out`, four lanes 64 bytes of a row. The ring keeps three boxes
 // a CTA in flight. Beside the streams the kernel has issue slots to spare only if a stage costs few
-// instructions: addresses advance by one stride, ring slots are unrolled, nothing is staged twice.
+// instructions: addresses advance by one stride, ring slots are unrolled, nothing is staged twice. 4096 x 14336,
+// rank 16: 42 us for 235 MB, 5.6 TB/s, 0.85 of the copy rate (five slots: 3 % slower, three CTAs of three: 4 %).
 template <int RT>
 struct UpdateShape {
     static constexpr int box = kTile * 128;
@@ -673,7 +682,8 @@ __global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, Pla
 // 128-byte rows, P's packed rows as boxes of the same kind. The reduction runs over the rows, so both
 // operands of D[column, rank] are read along their rows' contiguous side, as they lie: tcgen05 takes 2 x 128
 // columns x (first parts, second parts) a stage from one thread, and D stays in tensor memory until the
-// run comes to another adapter, when the two parts' sums are added. (With mma.sync, whose fragments cost
+// run comes to another adapter, when the two parts' sums are added. G and dB in one launch, 4096 x 4096 at rank 16: 17 us alone; dA and dX: 21
+// (101 MB, 4.8 TB/s). (With mma.sync, whose fragments cost
 // every warp transposed loads and registers, a stage took 1.2 us at rank 32: 29 us for G and dB at
 // 8192 x 2304.) The tiles are dealt evenly whatever their adapters: run k's sums for adapter a go to part[k + a]
 // (k and a only grow along the list, so no two share a place), or straight to `out` where the run has
@@ -902,6 +912,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_k
     }
 }
 
+// Latency again: 6 us alone for 4 + 4 MB of partial sums, of which its launch and look-ups are hidden.
 // The runs' partial sums, in run order, for the adapters whose tiles lie in several runs; zeros for those
 // without rows. y = 0: dA, 1: dB; z: adapters in turn.
 struct Sums {

