@@ -471,7 +471,8 @@ SS1_API int ss1_layernorm_backward_workspace(int64_t M, int64_t K, size_t* bytes
  *   workspace : device, 16-byte aligned, at least ss1_layernorm_backward_workspace bytes (0 for few
  *            elements); not needed where dweight and dbias are NULL. Calls that share one must be ordered.
  * The column sums are added in a fixed order: repeated calls give the same bits. Asynchronous.
- * A row whose statistics are not finite leaves NaN in all of dweight. Errors: as ss1_layernorm_forward; INVALID_ARG for a workspace that is too small.
+ * A row whose statistics are not finite leaves NaN in all of dweight. Errors: as ss1_layernorm_forward;
+ * INVALID_ARG for a workspace that is too small.
  */
 SS1_API int ss1_layernorm_backward(const void* dY, const void* X, const float* mean, const float* rstd, const void* weight,
                                    void* dX, void* dweight, void* dbias, int64_t M, int64_t K, int dtype, int w_dtype,
