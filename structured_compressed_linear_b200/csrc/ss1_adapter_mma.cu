@@ -29,8 +29,13 @@ namespace {
 using namespace op;
 using bf16 = __nv_bfloat16;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kPortableCluster = 8;
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
@@ -433,32 +438,29 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
     if (splits > 1) ptx::cluster_sync();
     else __syncthreads();
     const float f = scale ? scale[tile.adapter] : 1.0f;
-    const int pairs = tile.rows * (RT / 2);
-    for (int i = split * kThreads + tid; i < pairs; i += splits * kThreads) {
-        const int r = i / (RT / 2), c = (i % (RT / 2)) * 2;
-        float x = 0.0f, y = 0.0f;
-        if (splits > 1) {
-            for (int k = 0; k < splits; ++k) {
-                const uint32_t at = ptx::map_to_rank(part + r * S::pitch + c, k);
-                x += ptx::ld_cluster_f32(at);
-                y += ptx::ld_cluster_f32(at + 4);
-            }
-        } else {
-            x = part[r * S::pitch + c];
-            y = part[r * S::pitch + c + 1];
-        }
+    constexpr int kQuads = RT / 4;
+    for (int i = split * kThreads + tid; i < tile.rows * kQuads; i += splits * kThreads) {
+        const int r = i / kQuads, c = (i % kQuads) * 4;
+        float4 u[kPortableCluster];            // all asked for before the first is added
+#pragma unroll
+        for (int k = 0; k < kPortableCluster; ++k)
+            if (k < splits) u[k] = splits > 1 ? ld_cluster_f32x4(ptx::map_to_rank(part + r * S::pitch + c, k))
+                                              : *reinterpret_cast<const float4*>(part + r * S::pitch + c);
+        float v[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+        for (int k = 1; k < kPortableCluster; ++k)
+            if (k < splits) { v[0] += u[k].x; v[1] += u[k].y; v[2] += u[k].z; v[3] += u[k].w; }
         const int place = tile.first + r, m = row_at(plan, place, M);
-        if (H && m >= 0 && SS1_IN((int64_t)m * R, (int64_t)M * R, kSiteAdaH)) {
-            if (c < R) H[(int64_t)m * R + c] = x;
-            if (c + 1 < R) H[(int64_t)m * R + c + 1] = y;
-        }
-        x *= f;
-        y *= f;
-        uint32_t hi, lo;
-        split2(x, y, hi, lo);
-        if (SS1_SPAN_IN((int64_t)place * 2 * RT + RT + c, 2, (int64_t)M * 2 * RT, kSiteAdaG)) {
-            *reinterpret_cast<uint32_t*>(packed + (int64_t)place * 2 * RT + c) = hi;
-            *reinterpret_cast<uint32_t*>(packed + (int64_t)place * 2 * RT + RT + c) = lo;
+        if (H && m >= 0 && SS1_IN((int64_t)m * R, (int64_t)M * R, kSiteAdaH))
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + k < R) H[(int64_t)m * R + c + k] = v[k];
+        uint2 hi, lo;
+        split2(v[0] * f, v[1] * f, hi.x, lo.x);
+        split2(v[2] * f, v[3] * f, hi.y, lo.y);
+        if (SS1_SPAN_IN((int64_t)place * 2 * RT + RT + c, 4, (int64_t)M * 2 * RT, kSiteAdaG)) {
+            *reinterpret_cast<uint2*>(packed + (int64_t)place * 2 * RT + c) = hi;
+            *reinterpret_cast<uint2*>(packed + (int64_t)place * 2 * RT + RT + c) = lo;
         }
     }
     if (splits > 1) ptx::cluster_sync();   // nobody leaves while its sums are being read
@@ -1027,8 +1029,6 @@ cudaError_t launch_clusters(void (*fn)(P...), dim3 grid, int x, size_t smem, boo
     cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
-
-constexpr int kPortableCluster = 8;
 
 template <int RT>
 cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st) {
