@@ -20,6 +20,8 @@
 #include "ss1_adapter.cuh"
 #include "ptx_sm100.cuh"
 
+#include <algorithm>
+
 namespace ss1 {
 namespace ada {
 
@@ -453,20 +455,36 @@ __global__ void __launch_bounds__(256) tile_update_kernel(const float* __restric
     }
 }
 
-// D_a[c, r] = f * sum over adapter a's rows of U[m, c] P[m, r], for one share of the rows (blockIdx.z):
-// element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs of D, or of `out` where there is one share. A
-// thread is a column; 32 rows' P
-// lie in shared memory, and 32 rows of U are on their way at a time.
+// D_a[c, r] = f * sum over adapter a's rows of U[m, c] P[m, r], dA and dB in one launch (each CTA of either), for one
+// share of the rows (blockIdx.z): element (share, a, c, r) at share * n * C * R + a * C * R + c * cs + r * rs of D, or of
+// `out` where there is one share. A thread is a column; 32 rows' P lie in shared memory, and 32 rows of U are on
+// their way at a time.
 template <typename T>
-__global__ void __launch_bounds__(128) column_sums_kernel(const T* __restrict__ U, const float* __restrict__ P, PlanView plan,
-                                                          const float* __restrict__ scale, float* __restrict__ D, T* __restrict__ out,
-                                                          int64_t M, int C, int R, int n, int cs, int rs, int site_u) {
+struct ColumnSums {
+    const T* U;
+    const float* P;
+    const float* scale;
+    float* D;
+    T* out;
+    int C, cs, rs, shares, blocks, site;     // blocks: of 128 columns; 0: not wanted
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128) column_sums_kernel(const ColumnSums<T> da, const ColumnSums<T> db, PlanView plan, int64_t M, int R,
+                                                          int n) {
+    const bool second = (int)blockIdx.x >= da.blocks;
+    const ColumnSums<T>& d = second ? db : da;
+    const T* __restrict__ U = d.U;
+    const float* __restrict__ P = d.P;
+    const int C = d.C, cs = d.cs, rs = d.rs, shares = d.shares;
+    [[maybe_unused]] const int site_u = d.site;
+    if ((int)blockIdx.z >= shares) return;
     __shared__ __align__(16) float p[kSub][kRanks];
     __shared__ int64_t rows[kSub];
     const int a = blockIdx.y % n, r0 = (blockIdx.y / n) * kRanks, ranks = min(kRanks, R - r0);
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    const int c = ((int)blockIdx.x - (second ? da.blocks : 0)) * 128 + threadIdx.x;
     const int begin = plan.rows ? max(0, plan.first[a]) : 0, end = plan.rows ? min((int)M, plan.first[a + 1]) : (int)M;
-    const int shares = gridDim.z, per = (max(0, end - begin) + shares - 1) / shares;
+    const int per = (max(0, end - begin) + shares - 1) / shares;
     const int from = begin + (int)blockIdx.z * per, to = min(end, from + per);
     float s[kRanks];
 #pragma unroll
@@ -500,26 +518,26 @@ __global__ void __launch_bounds__(128) column_sums_kernel(const T* __restrict__ 
         }
     }
     if (c >= C) return;
-    const float f = scale ? scale[a] : 1.0f;
+    const float f = d.scale ? d.scale[a] : 1.0f;
     const int64_t size = (int64_t)n * C * R;
     const int64_t base = (int64_t)blockIdx.z * size + (int64_t)a * C * R + (int64_t)c * cs;
 #pragma unroll
     for (int r = 0; r < kRanks; ++r)
         if (r < ranks && SS1_IN(base + (int64_t)(r0 + r) * rs, size * shares, kSiteAdaPart)) {
-            if (shares == 1) out[base + (int64_t)(r0 + r) * rs] = from_f<T>(f * s[r]);
-            else D[base + (int64_t)(r0 + r) * rs] = f * s[r];
+            if (shares == 1) d.out[base + (int64_t)(r0 + r) * rs] = from_f<T>(f * s[r]);
+            else d.D[base + (int64_t)(r0 + r) * rs] = f * s[r];
         }
 }
 
-// out[i] = the shares' partial sums, added in share order.
+// The shares' partial sums of dA (blockIdx.y 0) and dB, added in share order; one share has written its result itself.
 template <typename T>
-__global__ void __launch_bounds__(256) add_shares_kernel(const float* __restrict__ part, T* __restrict__ out, int64_t size,
-                                                         int shares) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= size) return;
+__global__ void __launch_bounds__(256) add_shares_kernel(const ColumnSums<T> da, const ColumnSums<T> db, int R, int n) {
+    const ColumnSums<T>& d = blockIdx.y ? db : da;
+    const int64_t size = (int64_t)n * d.C * R, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (d.blocks == 0 || d.shares == 1 || i >= size) return;
     float s = 0.0f;
-    for (int k = 0; k < shares; ++k) s += part[k * size + i];
-    out[i] = from_f<T>(s);
+    for (int k = 0; k < d.shares; ++k) s += d.D[k * size + i];
+    d.out[i] = from_f<T>(s);
 }
 
 // A CTA takes one row while that reads no more than kAloneWork elements of A and B; beyond, 32 rows of an adapter
@@ -585,26 +603,28 @@ cudaError_t forward_general(const Call& c, const void* X, const void* Y, void* o
     return update<T>(c, H, c.B, c.scale, Y, out, c.N, c.R, 1, kSiteAdaB, st);
 }
 
+// dA = G^T X and dB = s dY^T H, whichever are wanted.
 template <typename T>
-cudaError_t column_sums(const Call& c, const void* U, const float* P, const float* scale, void* D, float* part, int64_t C, int cs,
-                        int rs, int site, cudaStream_t st) {
-    const int shares = general_shares(c.M, C, c.R, c.n);
-    const dim3 grid((unsigned)((C + 127) / 128), (unsigned)(c.n * ((c.R + kRanks - 1) / kRanks)), (unsigned)shares);
-    column_sums_kernel<T><<<grid, 128, 0, st>>>((const T*)U, P, c.plan, scale, part, (T*)D, c.M, (int)C, c.R, c.n, cs, rs, site);
-    const int64_t size = (int64_t)c.n * C * c.R;
-    if (shares > 1)      // one share writes D itself
-        add_shares_kernel<T><<<(unsigned)((size + 255) / 256), 256, 0, st>>>(part, (T*)D, size, shares);
+cudaError_t column_sums(const Call& c, const void* dY, const void* X, const float* H, const float* G, void* dA, void* dB, float* part_a,
+                        float* part_b, cudaStream_t st) {
+    const int sa = general_shares(c.M, c.K, c.R, c.n), sb = general_shares(c.M, c.N, c.R, c.n);
+    const ColumnSums<T> da{(const T*)X, G, nullptr, part_a, (T*)dA, (int)c.K, 1, (int)c.K, sa, dA ? (int)((c.K + 127) / 128) : 0, kSiteAdaX};
+    const ColumnSums<T> db{(const T*)dY, H, c.scale, part_b, (T*)dB, (int)c.N, c.R, 1, sb, dB ? (int)((c.N + 127) / 128) : 0, kSiteAdaY};
+    const int shares = std::max(dA ? sa : 1, dB ? sb : 1);
+    const dim3 grid((unsigned)(da.blocks + db.blocks), (unsigned)(c.n * ((c.R + kRanks - 1) / kRanks)), (unsigned)shares);
+    column_sums_kernel<T><<<grid, 128, 0, st>>>(da, db, c.plan, c.M, c.R, c.n);
+    const int64_t size = (int64_t)c.n * std::max(dA ? c.K : 0, dB ? c.N : 0) * c.R;
+    if (shares > 1) add_shares_kernel<T><<<dim3((unsigned)((size + 255) / 256), 2), 256, 0, st>>>(da, db, c.R, c.n);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t backward_general(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX,
-                             void* dA, void* dB, float* G, float* part, cudaStream_t st) {
+                             void* dA, void* dB, float* G, float* part_a, float* part_b, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (dX || dA) e = products<T>(c, dY, c.B, c.scale, G, c.N, c.R, 1, kSiteAdaY, kSiteAdaB, st);
     if (e == cudaSuccess && dX) e = update<T>(c, G, c.A, nullptr, dX_in, dX, c.K, 1, (int)c.K, kSiteAdaA, st);
-    if (e == cudaSuccess && dA) e = column_sums<T>(c, X, G, nullptr, dA, part, c.K, 1, (int)c.K, kSiteAdaX, st);
-    if (e == cudaSuccess && dB) e = column_sums<T>(c, dY, H, c.scale, dB, part, c.N, c.R, 1, kSiteAdaY, st);
+    if (e == cudaSuccess && (dA || dB)) e = column_sums<T>(c, dY, X, H, G, dA, dB, part_a, part_b, st);
     return e;
 }
 
@@ -620,11 +640,11 @@ bool sizes_ok(int64_t M, int64_t K, int64_t N, int R, int n, int dtype) {
 // does not depend on the alignment of the other pointers.
 struct Sizes {
     size_t plan;
-    size_t rows, part;                                  // general path: H or G; the partial sums of dA or dB
+    size_t rows, sums_a, sums_b;                        // general path: H or G; the partial sums of dA and dB
     size_t packed, wide_b, turned_a, part_a, part_b;    // tensor-core path
     size_t forward() const { return plan + (rows > packed + wide_b ? rows : packed + wide_b); }
     size_t backward() const {
-        const size_t a = rows + part, b = 2 * packed + wide_b + turned_a + part_a + part_b;
+        const size_t a = rows + sums_a + sums_b, b = 2 * packed + wide_b + turned_a + part_a + part_b;
         return plan + (a > b ? a : b);
     }
 };
@@ -633,8 +653,8 @@ Sizes workspace_of(int64_t M, int64_t K, int64_t N, int R, int n) {
     s.plan = align_up(plan_bytes(M, n));
     s.rows = align_up((size_t)M * R * sizeof(float));
     const size_t a = (size_t)n * K * R, b = (size_t)n * N * R;
-    const size_t ga = general_shares(M, K, R, n) * a, gb = general_shares(M, N, R, n) * b;
-    s.part = align_up((ga > gb ? ga : gb) * sizeof(float));
+    s.sums_a = align_up(general_shares(M, K, R, n) * a * sizeof(float));
+    s.sums_b = align_up(general_shares(M, N, R, n) * b * sizeof(float));
     s.packed = align_up((size_t)M * mma_rank(R) * 2 * sizeof(uint16_t));
     s.wide_b = R % 8 ? align_up((size_t)n * N * ((R + 7) / 8 * 8) * sizeof(uint16_t)) : 0;
     s.turned_a = align_up((size_t)n * K * ((R + 7) / 8 * 8) * sizeof(uint16_t));
@@ -820,10 +840,11 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
         return SS1_OK;
     }
     float* G = reinterpret_cast<float*>(ws + s.plan);
-    float* part = reinterpret_cast<float*>(ws + s.plan + s.rows);
+    float* part_a = reinterpret_cast<float*>(ws + s.plan + s.rows);
+    float* part_b = reinterpret_cast<float*>(ws + s.plan + s.rows + s.sums_a);
     if (err == cudaSuccess)
-        err = ad->dtype == SS1_DTYPE_BF16 ? backward_general<__nv_bfloat16>(c, dY, X, H, dX_in, dX, dA, dB, G, part, st)
-                                          : backward_general<float>(c, dY, X, H, dX_in, dX, dA, dB, G, part, st);
+        err = ad->dtype == SS1_DTYPE_BF16 ? backward_general<__nv_bfloat16>(c, dY, X, H, dX_in, dX, dA, dB, G, part_a, part_b, st)
+                                          : backward_general<float>(c, dY, X, H, dX_in, dX, dA, dB, G, part_a, part_b, st);
     if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
     return SS1_OK;
 }
