@@ -13,8 +13,8 @@
 // writes each element once: these two keep mma.sync and sums in registers.
 //
 // Ranks are padded to 16, 32, 64 or 128 (RT). Whole passes, us as graph replays beside what their bytes take at the measured
-// 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 59 (41.7); 16384 x 4096 x 4096: 86 (61.8). Backward, one
-// adapter of 4096 x 4096 x 4096, rank 16: 39 (20.6), rank 64: 56, rank 128: 99; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
+// 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 58 (41.7); 16384 x 4096 x 4096: 85 (61.8). Backward, one
+// adapter of 4096 x 4096 x 4096, rank 16: 39 (20.6), rank 64: 55, rank 128: 97; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
 //
 // P between the kernels: rows in plan order, [2][RT] bf16 each: the value rounded to bf16, and
 // what that left out, rounded again (2^-17 of the value is lost). The products with both parts are
@@ -435,6 +435,7 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
         }
     }
     wait_for_previous();
+    if (TRANS) let_next_start();           // second_gradients_kernel: what prepare_kernel wrote is complete here
     if (splits > 1) ptx::cluster_sync();
     else __syncthreads();
     const float f = scale ? scale[tile.adapter] : 1.0f;
@@ -506,7 +507,7 @@ struct Update {
 
 template <int RT>
 __device__ __forceinline__ void update_role(const Update& d, const PlanView& plan, const Tile& tile, int split, uint8_t* raw, int M,
-                                            int R, int n, bool table_is_new) {
+                                            int R, int n) {
     using S = UpdateShape<RT>;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, C = d.C;
     const int chunks = (C + 63) / 64, per = (chunks + d.splits - 1) / d.splits;
@@ -584,7 +585,6 @@ __device__ __forceinline__ void update_role(const Update& d, const PlanView& pla
         }
         ptx::cp_async_commit();
     };
-    if (table_is_new) wait_for_previous();
 #pragma unroll
     for (int s = 0; s < S::stages - 1; ++s) load(from + s < to, s);
     const int g = lane / 4, t4 = lane % 4;
@@ -674,7 +674,7 @@ __device__ __forceinline__ void update_role(const Update& d, const PlanView& pla
 template <int RT>
 __global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
-    update_role<RT>(d, plan, tile_of(plan, blockIdx.y, M), blockIdx.x, raw, M, R, n, false);
+    update_role<RT>(d, plan, tile_of(plan, blockIdx.y, M), blockIdx.x, raw, M, R, n);
     wait_for_previous();   // also in CTAs that left early: this grid never ends before the one before it
 }
 
@@ -724,7 +724,7 @@ __device__ __forceinline__ int tiles_a_run(const PlanView& plan, int n, int M, i
 
 template <int RT>
 __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& plan, int range, int run, uint8_t* raw, TensorState& ts,
-                                             int M, int R, int n) {
+                                             int M, int R, int n, bool packed_is_new) {
     using S = ColumnsShape<RT>;
     static_assert(S::stages <= kSlots, "a barrier a slot");
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
@@ -753,9 +753,9 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
     };
     Tile now = tile_at(t0), next = tile_at(t0 + 1), after = tile_at(t0 + 2);   // of the stage to be loaded
     int now_row = row_of(now), next_row = row_of(next);
-    auto load = [&](int step, int slot) {
+    auto load_u = [&](int step, int slot) {
         if (step < steps) {
-            const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
+            const uint32_t su = base + slot * S::stage;
             const int k = step % kColSteps;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -764,27 +764,40 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
                 const bool ok = m >= 0 && cok && SS1_SPAN_IN(at, 8, (int64_t)M * C, kSiteAdaX);
                 copy16(su + udst[i], ok ? d.U + at : d.U, ok);
             }
+        }
+    };
+    auto load_p = [&](const Tile& tile, int step, int slot) {
+        if (step < steps) {
+            const uint32_t sp = base + slot * S::stage + S::u_bytes;
+            const int k = step % kColSteps;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int e = tid + i * kThreads, r = e / (RT / 4), c = (e % (RT / 4)) * 8;
-                const int64_t at = (int64_t)(now.first + k * kColRows + r) * 2 * RT + c;
-                const bool ok = k * kColRows + r < now.rows && SS1_SPAN_IN(at, 8, (int64_t)M * 2 * RT, kSiteAdaG);
+                const int64_t at = (int64_t)(tile.first + k * kColRows + r) * 2 * RT + c;
+                const bool ok = k * kColRows + r < tile.rows && SS1_SPAN_IN(at, 8, (int64_t)M * 2 * RT, kSiteAdaG);
                 if (kPieces % kThreads == 0 || e < kPieces)
                     copy16(sp + c / 64 * S::box + r * 128 + (((c / 8 % 8) ^ (r & 7)) << 4), ok ? d.packed + at : d.packed, ok);
-            }
-            if (k == kColSteps - 1) {
-                now = next;
-                now_row = next_row;
-                next = after;
-                next_row = row_of(next);
-                after = tile_at(t0 + step / kColSteps + 3);
             }
         }
         ptx::cp_async_commit();
     };
+    auto advance = [&](int step) {
+        if (step < steps && step % kColSteps == kColSteps - 1) {
+            now = next;
+            now_row = next_row;
+            next = after;
+            next_row = row_of(next);
+            after = tile_at(t0 + step / kColSteps + 3);
+        }
+    };
 
     int adapter = now.adapter, next_adapter = adapter;
-    for (int s = 0; s < S::stages - 1; ++s) load(s, s);
+    static_assert(S::stages - 1 <= kColSteps, "the first stages lie in the first tile");
+    const Tile head = now;
+    for (int s = 0; s < S::stages - 1; ++s) load_u(s, s);
+    if (packed_is_new) wait_for_previous();      // P is the previous kernel's, U and the plan are not
+    for (int s = 0; s < S::stages - 1; ++s) load_p(head, s, s);
+    for (int s = 0; s < S::stages - 1; ++s) advance(s);
     tensor_begin(ts, S::columns);
     const uint32_t tmem = ts.tmem;
     constexpr uint32_t kInstr = idesc_mn(2 * RT, true, true);
@@ -863,7 +876,9 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
         fresh = false;
         const int last = slot == 0 ? S::stages - 1 : slot - 1;        // the slot of the step before: loaded again once read
         if (step > 0) tensor_wait(ts, last, ((step - 1) / S::stages) & 1);
-        load(step + S::stages - 1, last);
+        load_u(step + S::stages - 1, last);
+        load_p(now, step + S::stages - 1, last);
+        advance(step + S::stages - 1);
         slot = slot == S::stages - 1 ? 0 : slot + 1;
     }
     ptx::cp_async_wait<0>();
@@ -882,17 +897,18 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) first_gradients_ke
                                                                                      PlanView plan, int M, int R, int n) {
     extern __shared__ uint8_t raw[];
     __shared__ TensorState ts;
-    let_next_start();             // its successors wait first thing
     if ((int)blockIdx.y < tiles) {
         products_role<RT, true>(g, plan, blockIdx.y, raw, ts, M, R, n);
     } else {
         wait_for_previous();      // the packed H
+        let_next_start();
         const int k = ((int)blockIdx.y - tiles) * gridDim.x + blockIdx.x, ranges = (db.C + kColCols - 1) / kColCols;
-        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, ts, M, R, n);
+        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, ts, M, R, n, false);
     }
 }
 
-// dA and dX in one launch: both need G. CTAs 0 .. na - 1 take dA, the rest dX.
+// dA and dX in one launch: both need G, but their first loads, of X, dX and A, do not wait for it (300 x 1024 x 1024 16.2 -> 15.3
+// us, 8192 x 768 x 2304 47.1 -> 46.5, 4096 x 4096 x 14336 63.8 -> 65.4). CTAs 0 .. na - 1 take dA, the rest dX.
 template <int RT>
 constexpr int second_smem() {
     return ColumnsShape<RT>::smem > UpdateShape<RT>::smem ? ColumnsShape<RT>::smem : UpdateShape<RT>::smem;
@@ -901,17 +917,20 @@ constexpr int second_smem() {
 template <int RT>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_kernel(const Columns da, int na, const Update dx,
                                                                                       PlanView plan, int M, int R, int n) {
+    // CTAs of both launches may share an SM: their tensor memory has room, or shared memory for one of them only
+    static_assert(RT <= 64 ? 2 * ColumnsShape<RT>::columns <= 512 && first_smem<RT>() + 2 * second_smem<RT>() > 232448
+                           : first_smem<RT>() + second_smem<RT>() > 232448, "512 columns an SM");
     extern __shared__ uint8_t raw[];
     __shared__ TensorState ts;
-    let_next_start();
-    wait_for_previous();
+    let_next_start();      // its successors wait first thing
     const int i = blockIdx.x;
     if (i < na) {
         const int ranges = (da.C + kColCols - 1) / kColCols;
-        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, ts, M, R, n);
+        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, ts, M, R, n, true);
     } else {
-        update_role<RT>(dx, plan, tile_of(plan, (i - na) / dx.splits, M), (i - na) % dx.splits, raw, M, R, n, true);
+        update_role<RT>(dx, plan, tile_of(plan, (i - na) / dx.splits, M), (i - na) % dx.splits, raw, M, R, n);
     }
+    wait_for_previous();   // also in CTAs that left early
 }
 
 // Latency again: 6 us alone for 4 + 4 MB of partial sums, of which its launch and look-ups are hidden.
