@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, Pla
 // 128-byte rows, P's packed rows as boxes of the same kind. The reduction runs over the rows, so both
 // operands of D[column, rank] are read along their rows' contiguous side, as they lie: tcgen05 takes 2 x 128
 // columns x (first parts, second parts) a stage from one thread, and D stays in tensor memory until the
-// run comes to another adapter, when the two parts' sums are added. G and dB in one launch, 4096 x 4096 at rank 16: 17 us alone; dA and dX: 21
-// (101 MB, 4.8 TB/s). (With mma.sync, whose fragments cost
+// run comes to another adapter, when the two parts' sums are added. G and dB in one launch, 4096 x 4096 at rank 16: 17.7 us alone; dA and dX: 20.4
+// (101 MB, 4.9 TB/s). (With mma.sync, whose fragments cost
 // every warp transposed loads and registers, a stage took 1.2 us at rank 32: 29 us for G and dB at
 // 8192 x 2304.) The tiles are dealt evenly whatever their adapters: run k's sums for adapter a go to part[k + a]
 // (k and a only grow along the list, so no two share a place), or straight to `out` where the run has
