@@ -14,7 +14,7 @@
 //
 // Ranks are padded to 16, 32, 64 or 128 (RT). Whole passes, us as graph replays beside what their bytes take at the measured
 // 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 58 (41.7); 16384 x 4096 x 4096: 85 (61.8). Backward, one
-// adapter of 4096 x 4096 x 4096, rank 16: 39 (20.6), rank 64: 55, rank 128: 97; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
+// adapter of 4096 x 4096 x 4096, rank 16: 38 (20.6), rank 64: 55, rank 128: 97; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
 //
 // P between the kernels: rows in plan order, [2][RT] bf16 each: the value rounded to bf16, and
 // what that left out, rounded again (2^-17 of the value is lost). The products with both parts are
@@ -697,7 +697,7 @@ struct ColumnsShape {
     static constexpr int box = kColRows * 128;
     static constexpr int u_bytes = kColCols / 64 * box, p_boxes = (2 * RT + 63) / 64;
     static constexpr int stage = u_bytes + p_boxes * box;
-    static constexpr int stages = RT <= 32 ? 5 : (RT <= 64 ? 4 : 3);
+    static constexpr int stages = RT <= 64 ? 4 : 3;
     static constexpr int smem = stages * stage + 1024;
     static constexpr uint32_t columns = 2 * 2 * RT;            // of tensor memory
 };
