@@ -551,11 +551,16 @@ SS1_API int ss1_adapter_backward(const ss1_adapters* adapters, const void* dY, c
  * each float32 operation rounded on its own. States of 8 bits: blocks of SS1_ADAMW_BLOCK consecutive
  * elements (the last one of a tensor may be shorter) share one float scale, the smallest power of
  * two from 2^-126 on that brings the block's largest magnitude to 448 or below; held are OCP FP8
- * E4M3 codes of m / scale and of sqrt(v) / scale (rounded to nearest even, a positive root at least
- * to the smallest code; a NaN is held as NaN and does not count for the scale, an infinity makes it
- * 2^120). The step uses the new moments before they are rounded.
+ * E4M3 codes of m / scale and of sqrt(v) / scale (a positive root at least the smallest code; a NaN
+ * is held as NaN and does not count for the scale, an infinity makes it 2^120). Steps 1 ..
+ * SS1_ADAMW_NEAREST round to nearest even; later ones to one of the two codes around the value, to
+ * each with the probability that leaves the value as it is on average, by a hash of the step number and the
+ * element's place: rounded to nearest, a moment that moves by less than half a code a step would stand
+ * still. So a parameter's steps must be numbered 1, 2, ... . The same step on the same state gives the
+ * same bits. The step uses the new moments before they are rounded.
  */
 #define SS1_ADAMW_BLOCK 256
+#define SS1_ADAMW_NEAREST 10
 #define SS1_ADAMW_FACTORS 9
 
 typedef struct {
@@ -581,16 +586,27 @@ typedef struct {
  *   tensors : host array, read during the call. Tensors must not overlap one another. numel == 0
  *             is allowed (pointers unused).
  *   state_bits : 32 or 8, for all tensors. All-zero bytes are a valid start in both.
- *   hyper   : host; unused where device_factors is given.
+ *   hyper   : host; unused where device_factors is given (but see device_step).
  *   device_factors : NULL, or device float [SS1_ADAMW_FACTORS] as ss1_adamw_factors writes them, read
  *             when the step runs: a captured step can be replayed with new factors.
  * Up to 440 tensors run in one launch. Everything is checked before the first launch: a refused
  * call has changed nothing. Asynchronous. Errors: INVALID_ARG (sizes, types, NULL pointers, a master
  * copy beside float32 parameters, hyper-parameters out of range: 0 <= beta < 1, eps >= 0, step >= 1,
- * finite), MISALIGNED (a pointer not aligned to its element), CUDA.
+ * finite; 8-bit states with device_factors, which need ss1_adamw_step_ex), MISALIGNED (a pointer not
+ * aligned to its element), CUDA.
  */
 SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t count, int state_bits, const ss1_adamw_hyper* hyper,
                            const float* device_factors, void* stream);
+
+/*
+ * ss1_adamw_step_ex -- ss1_adamw_step with the step's number on the device, for captured steps.
+ *   device_step : NULL, or device int64, read when the step runs, with device_factors beside it: the number that
+ *             8-bit states are rounded by is *device_step, plus hyper->step where hyper is given. It
+ *             has to differ from replay to replay (count it up in the graph); 8-bit states need it with device_factors.
+ * Errors: as ss1_adamw_step; INVALID_ARG for device_step without device_factors.
+ */
+SS1_API int ss1_adamw_step_ex(const ss1_adamw_tensor* tensors, int64_t count, int state_bits, const ss1_adamw_hyper* hyper,
+                              const float* device_factors, const int64_t* device_step, void* stream);
 
 /*
  * ss1_adamw_factors -- the step's factors in float32, to host memory out[SS1_ADAMW_FACTORS] (no device

@@ -12,13 +12,23 @@
 // least the smallest code: rounded to 0 it would make the next update m / eps. The update itself
 // uses the unrounded new moments.
 //
+// Codes lie 6 to 12 % apart, and step t moves a moment by about 1 / t of itself, later by 1 - beta. Rounded to the nearest
+// code a moment stands still once that is less than half the distance. So only the first SS1_ADAMW_NEAREST
+// steps take the nearest code; a later one takes either neighbour, the farther one as often as the value lies towards
+// it: the held value then follows the moment on average. What decides is a hash of step and element, so a step repeated
+// gives the same bits. 2000 steps at the default betas, constant / normal gradients: r.m.s. update 1.01 / 1.02 of float32
+// moments' (always nearest: 5.1 / 2.3, the held root 0.12 / 0.39 of the true one). Nearest up to 10 steps: held roots 0.98 to
+// 1.04 of the true ones, spread 0.07 at most, as with either neighbour from the start; up to 16: 0.85.
+//
 // Memory-bound: bf16 weights with a float32 master copy move 28 bytes an element with float32
 // moments, 16 with 8-bit ones. Every float32 operation is rounded on its own (no fused multiply-
 // add), so that the codes are those of the same formula written with elementwise operations.
 //
-// 30 M bf16 weights with master copies: float32 moments 134 us (840 MB at 6.3 TB/s, 0.96 of the copy rate); 8 bits 93 us
-// (482 MB, 5.2 TB/s, 0.79; 106 with three CTAs an SM), where the issue slots of each element's root and quotient
-// (57 % busy) and the loads that 64 registers a thread keep in flight bound it together.
+// 30 M bf16 weights with master copies: float32 moments 135 us (840 MB at 6.2 TB/s, 0.95 of the copy rate); 8 bits 93 us
+// while codes are the nearest (482 MB, 5.2 TB/s, 0.79), where the issue slots of each element's root and quotient (57 %
+// busy) and the loads that 64 registers a thread keep in flight bound it together, and 115 us past that (4.2 TB/s, 0.64),
+// where random bits and neighbours add to the issue slots. Each rounding has a loop of its own: one loop with the
+// choice inside took 40 % longer for both.
 #include "ss1_ops.cuh"
 
 #include <cuda_fp16.h>
@@ -34,6 +44,7 @@ using namespace op;
 constexpr int kBlock = 256;              // elements of one scale: one warp, eight a lane
 constexpr int kWarps = 8;
 constexpr int kChunk = kBlock * kWarps * 4;   // elements of a CTA: four blocks a warp
+constexpr int64_t kNearest = SS1_ADAMW_NEAREST;
 
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kAligned = 4 };
 
@@ -143,21 +154,53 @@ __device__ __forceinline__ float block_scale(const F2 (&f)[4]) {
     return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
 
-__device__ __forceinline__ uint2 encode8(const F2 (&f)[4], float scale) {
+// Random bits: two rounds of xor-shift and product (odd constants, from the golden ratio and the root of 3) on the lane's
+// number in the tensor, by a key of the step; a linear congruence leads through the lane's eight elements.
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = (x ^ x >> 16) * 0x9E3779B9u;
+    x = (x ^ x >> 15) * 0xBB67AE85u;
+    return x ^ x >> 16;
+}
+__device__ __forceinline__ uint32_t step_key(int64_t step) {
+    return mix((uint32_t)step * 0x9E3779B9u + (uint32_t)(step >> 32) * 0xBB67AE85u + 0x3C6EF373u);
+}
+__device__ __forceinline__ uint32_t lane_bits(uint32_t key, int64_t number) {
+    return mix((uint32_t)number ^ (key + (uint32_t)(number >> 32) * 0x9E3779B9u));
+}
+__device__ __forceinline__ uint32_t next_bits(uint32_t x) { return x * 0xB7E15165u + 0x243F6A89u; }
+
+// One of the two E4M3 values around x, |x| <= 448: the one away from 0 for as many of the 2^20 values of `bits` as x lies of the
+// 2^20 parts of the way towards it. A code keeps a float's upper 3 bits of fraction, so the other 20 plus `bits`
+// carry into them that often. Below 2^-6 codes lie 2^-9 apart, as they do from there to 2^-5.
+__device__ __forceinline__ float neighbour(float x, uint32_t bits) {
+    const float shift = fabsf(x) < 0x1p-6f ? copysignf(0x1p-6f, x) : 0.0f;
+    const float y = __uint_as_float((__float_as_uint(x + shift) + bits) & 0xFFF00000u) - shift;
+    return x == x ? y : x;
+}
+
+// The nearest codes, or (DITHER) neighbours by the upper 20 bits of each element's random word times TURN.
+template <bool DITHER, uint32_t TURN>
+__device__ __forceinline__ uint2 encode8(const F2 (&f)[4], float scale, uint32_t bits) {
     // 1 / scale, exactly: scale = 2^e with -126 <= e <= 121
     const F2 by = F2::both(__uint_as_float((254u << 23) - __float_as_uint(scale)));
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const F2 x = f[i] * by;   // exact but for results below 2^-126
+        F2 x = f[i] * by;   // exact but for results below 2^-126
+        if (DITHER) {
+            const uint32_t second = next_bits(bits);
+            x = F2::of(neighbour(x.lo(), bits * TURN >> 12), neighbour(x.hi(), second * TURN >> 12));
+            bits = next_bits(second);
+        }
         w[i / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.lo(), x.hi()), __NV_SATFINITE, __NV_E4M3) << (16 * (i % 2));
     }
     return make_uint2(w[0], w[1]);
 }
 
 // Eight elements of one lane: `at` in the tensor, `block` their block, whose 32 lanes come here together.
-template <int BITS, bool WHOLE>
-__device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Factors& f, F2 none, int64_t at, int n, int64_t block, int lane) {
+template <int BITS, bool DITHER, bool WHOLE>
+__device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Factors& f, F2 none, uint32_t key, int64_t at, int n,
+                                        int64_t block, int lane) {
     F2 g[4], p[4], m[4], v[4], root[4];
     uint2 mc, vc;
     float ms, vs;
@@ -208,8 +251,9 @@ __device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Fa
     }
     ms = block_scale(m);
     vs = block_scale(root);
-    mc = encode8(m, ms);
-    vc = encode8(root, vs);
+    const uint32_t bits = lane_bits(key, block * 32 + lane);
+    mc = encode8<DITHER, 0xBB67AE85u>(m, ms, bits);
+    vc = encode8<DITHER, 1>(root, vs, bits);
     // a positive root that rounded to code 0 takes code 1; most words have no zero byte
     uint32_t w[2] = {vc.x, vc.y};
 #pragma unroll
@@ -229,9 +273,26 @@ __device__ __forceinline__ void update8(const Entry& t, uint32_t flags, const Fa
     }
 }
 
+template <int BITS, bool DITHER>
+__device__ __forceinline__ void update_chunk(const Entry& t, uint32_t flags, const Factors& f, F2 none, uint32_t key, int64_t start, int warp,
+                                             int lane) {
+#pragma unroll 1
+    for (int k = warp; k < kChunk / kBlock; k += kWarps) {
+        const int64_t block = start / kBlock + k, at = block * kBlock + lane * 8;
+        if (block * kBlock >= t.n) break;
+        if ((flags & kAligned) && (block + 1) * kBlock <= t.n && SS1_SPAN_IN(at, 8, t.n, kSiteAdamTensor)) {
+            update8<BITS, DITHER, true>(t, flags, f, none, key, at, 8, block, lane);
+        } else {
+            const int64_t left = t.n - at;
+            update8<BITS, DITHER, false>(t, flags, f, none, key, left > 0 ? at : 0, left >= 8 ? 8 : (left > 0 ? (int)left : 0), block, lane);
+        }
+    }
+}
+
 template <int N, int BITS>
 __global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_constant__ Table<N> table, const Factors host,
-                                                            const float* __restrict__ device, float minus_zero) {
+                                                            const float* __restrict__ device, int64_t step,
+                                                            const int64_t* __restrict__ device_step, float minus_zero) {
     wait_for_previous();
     const F2 none = F2::both(minus_zero);
     Factors f = host;
@@ -239,6 +300,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_cons
         float* to = reinterpret_cast<float*>(&f);
 #pragma unroll
         for (int i = 0; i < kFactors; ++i) to[i] = __ldg(device + i);
+    }
+    bool dither = false;
+    uint32_t key = 0;
+    if (BITS == 8) {
+        if (device_step) step += __ldg(device_step);
+        dither = step > kNearest;
+        key = step_key(step);
     }
     // the tensor whose chunks contain this CTA's: the last one that starts at or before it
     int lo = 0, hi = table.count - 1;
@@ -251,23 +319,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4) adamw_kernel(const __grid_cons
     const uint32_t flags = table.flags[lo];
     const int64_t start = (int64_t)((int)blockIdx.x - table.first[lo]) * kChunk;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-#pragma unroll 1
-    for (int k = warp; k < kChunk / kBlock; k += kWarps) {
-        const int64_t block = start / kBlock + k, at = block * kBlock + lane * 8;
-        if (block * kBlock >= t.n) break;
-        if ((flags & kAligned) && (block + 1) * kBlock <= t.n && SS1_SPAN_IN(at, 8, t.n, kSiteAdamTensor)) {
-            update8<BITS, true>(t, flags, f, none, at, 8, block, lane);
-        } else {
-            const int64_t left = t.n - at;
-            update8<BITS, false>(t, flags, f, none, left > 0 ? at : 0, left >= 8 ? 8 : (left > 0 ? (int)left : 0), block, lane);
-        }
-    }
+    if (BITS == 8 && dither) update_chunk<BITS, BITS == 8>(t, flags, f, none, key, start, warp, lane);
+    else update_chunk<BITS, false>(t, flags, f, none, key, start, warp, lane);
 }
 
 template <int N>
 cudaError_t launch(const ss1_adamw_tensor* tensors, int64_t count, int bits, const Factors& f,
-                   const float* device, cudaStream_t st) {
-    static_assert(sizeof(Table<N>) + sizeof(Factors) + 24 <= 32764, "kernel parameters");
+                   const float* device, int64_t step, const int64_t* device_step, cudaStream_t st) {
+    static_assert(sizeof(Table<N>) + sizeof(Factors) + 48 <= 32764, "kernel parameters");
     Table<N> table;
     table.count = 0;
     int64_t chunks = 0;
@@ -297,7 +356,7 @@ cudaError_t launch(const ss1_adamw_tensor* tensors, int64_t count, int bits, con
     cfg.numAttrs = 1;
     Factors factors = f;
     float minus_zero = -0.0f;
-    void* args[] = {&table, &factors, &device, &minus_zero};
+    void* args[] = {&table, &factors, &device, &step, &device_step, &minus_zero};
     return cudaLaunchKernelExC(&cfg, bits == 32 ? reinterpret_cast<const void*>(&adamw_kernel<N, 32>)
                                                 : reinterpret_cast<const void*>(&adamw_kernel<N, 8>), args);
 }
@@ -340,9 +399,17 @@ extern "C" SS1_API int ss1_adamw_factors(const ss1_adamw_hyper* hyper, float* ou
 
 extern "C" SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t count, int state_bits,
                                       const ss1_adamw_hyper* hyper, const float* device_factors, void* stream) {
+    return ss1_adamw_step_ex(tensors, count, state_bits, hyper, device_factors, nullptr, stream);
+}
+
+extern "C" SS1_API int ss1_adamw_step_ex(const ss1_adamw_tensor* tensors, int64_t count, int state_bits, const ss1_adamw_hyper* hyper,
+                                         const float* device_factors, const int64_t* device_step, void* stream) {
     if (count < 0 || (count > 0 && !tensors) || (state_bits != 32 && state_bits != 8)) return SS1_ERR_INVALID_ARG;
     if (!device_factors && !hyper_ok(hyper)) return SS1_ERR_INVALID_ARG;
-    if (!aligned(device_factors, 4)) return SS1_ERR_MISALIGNED;
+    if (device_step && !device_factors) return SS1_ERR_INVALID_ARG;
+    if (!aligned(device_factors, 4) || !aligned(device_step, 8)) return SS1_ERR_MISALIGNED;
+    // rounding by a step number that a replayed graph repeats would hold its moments still
+    if (state_bits == 8 && device_factors && !device_step) return SS1_ERR_INVALID_ARG;
     // everything is checked before the first launch, so that a refused call has changed nothing
     for (int64_t i = 0; i < count; ++i) {
         const ss1_adamw_tensor& t = tensors[i];
@@ -359,6 +426,7 @@ extern "C" SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t c
     }
     Factors f = {};
     if (!device_factors) f = factors(*hyper);
+    const int64_t step = hyper ? hyper->step : 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int64_t at = 0; at < count;) {
         // as many tensors as one launch takes, and no more chunks than its grid can count
@@ -368,8 +436,8 @@ extern "C" SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t c
             if (end > at && chunks + c > 0x7FFFFFFF) break;
             chunks += c;
         }
-        const cudaError_t e = end - at <= kSmall ? launch<kSmall>(tensors + at, end - at, state_bits, f, device_factors, st)
-                                                 : launch<kLarge>(tensors + at, end - at, state_bits, f, device_factors, st);
+        const cudaError_t e = end - at <= kSmall ? launch<kSmall>(tensors + at, end - at, state_bits, f, device_factors, step, device_step, st)
+                                                 : launch<kLarge>(tensors + at, end - at, state_bits, f, device_factors, step, device_step, st);
         if (e != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
         at = end;
     }

@@ -25,8 +25,10 @@ from .ss1 import _check, _dtype_code, lib
 #: Limits of the adapters (SS1_ADAPTER_MAX_RANK, SS1_ADAPTER_MAX_COUNT in include/ss1.h).
 ADAPTER_MAX_RANK = 128
 ADAPTER_MAX_COUNT = 1024
-#: Elements that share one scale of an 8-bit AdamW state, and the step's factors (SS1_ADAMW_*).
+#: Elements that share one scale of an 8-bit AdamW state, the last step that rounds such states to the nearest
+#: code, and the step's factors (SS1_ADAMW_*).
 ADAMW_BLOCK = 256
+ADAMW_NEAREST = 10
 ADAMW_FACTORS = 9
 
 
@@ -366,12 +368,20 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
                betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                grad_scale: float = 1.0, master: Optional[Sequence[Optional[torch.Tensor]]] = None,
                scales: Optional[Tuple[Sequence[torch.Tensor], Sequence[torch.Tensor]]] = None,
-               factors: Optional[torch.Tensor] = None) -> None:
+               factors: Optional[torch.Tensor] = None, device_step: Optional[torch.Tensor] = None) -> None:
     """One AdamW step over all tensors, in place (ss1_adamw_step). params and grads: bf16 or float32, each
     tensor by itself. exp_avg and exp_avg_sq: float32; with `scales` = (of the first moment, of the
-    root of the second one), float32 [ceil(numel / ADAMW_BLOCK)] each, uint8 E4M3 codes instead.
+    root of the second one), float32 [ceil(numel / ADAMW_BLOCK)] each, uint8 E4M3 codes instead. `step` numbers
+    the parameters' steps from 1 on: past ADAMW_NEAREST, codes are rounded up or down by a hash of it.
     master: float32 copies of bf16 params, which the step then reads and writes (None: has none). factors: float32
-    CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale."""
+    CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale. device_step: int64 CUDA tensor [1],
+    the step's number beside `factors`, read on the device too; 8-bit states with factors need it."""
+    _adamw(params, grads, exp_avg, exp_avg_sq, 0 if device_step is not None else step, lr, betas, eps, weight_decay, grad_scale,
+           master, scales, factors, device_step)
+
+
+def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay, grad_scale, master, scales, factors, device_step):
+    """adamw_step; with a device_step, `step` is added to it."""
     n = len(params)
     if n == 0:
         return
@@ -407,8 +417,12 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
         table["sq_scale"] = _like("scales[1]", scales[1], blocks, device, _F32)
     if factors is not None:
         _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
+    if device_step is not None:
+        _tensor("device_step", device_step, (1,), torch.int64, device)
+    if (device_step is not None) > (factors is not None) or (bits == 8 and factors is not None and device_step is None):
+        raise ValueError("device_step goes with factors, and 8-bit states with factors need it")
     hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
-    _call(device, lib().ss1_adamw_step, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors))
+    _call(device, lib().ss1_adamw_step_ex, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), _ptr(device_step))
 
 
 class AdamW:
