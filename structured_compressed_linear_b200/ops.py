@@ -427,9 +427,13 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
 
 class AdamW:
     """AdamW over a list of parameters: holds the states and calls adamw_step with each parameter's .grad
-    (parameters without one are left as they are).
+    (parameters without one are left as they are). Every parameter has a step number of its own, so one that
+    gets its first gradient late starts with the bias corrections of step 1.
 
-    state_bits: 32 or 8. master: float32 copies of the bf16 parameters."""
+    state_bits: 32 or 8. master: float32 copies of the bf16 parameters.
+
+    In a CUDA graph: capture step(factors=...) and write adamw_factors of the next step number to `factors`
+    before each replay. The captured steps count their replays on the device."""
 
     def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
@@ -442,7 +446,11 @@ class AdamW:
             if any(q is p for q in self.params[:i]):
                 raise ValueError(f"params[{i}] is in the list twice")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
-        self.state_bits, self.steps = state_bits, 0
+        self.state_bits = state_bits
+        # steps that were run by the host, and replays of captured steps (of the parameters in _captured)
+        self._counts = [0] * len(self.params)
+        self._captured: Optional[List[int]] = None
+        self._replays = self.params[0].new_zeros(1, dtype=torch.int64, requires_grad=False) if self.params else None
         state = torch.float32 if state_bits == 32 else torch.uint8
         self.exp_avg = [torch.zeros_like(p, dtype=state) for p in self.params]
         self.exp_avg_sq = [torch.zeros_like(p, dtype=state) for p in self.params]
@@ -456,28 +464,75 @@ class AdamW:
         for p in self.params:
             p.grad = None
 
+    def counts(self) -> List[int]:
+        """Each parameter's number of steps. Waits for the device once a step was captured."""
+        if self._captured is None:
+            return list(self._counts)
+        replays, captured = int(self._replays), set(self._captured)
+        return [c + replays if i in captured else c for i, c in enumerate(self._counts)]
+
+    @property
+    def steps(self) -> int:
+        """The largest of the parameters' step numbers."""
+        return max(self.counts(), default=0)
+
     @torch.no_grad()
     def step(self, grad_scale: float = 1.0, factors: Optional[torch.Tensor] = None,
              stream: Optional[torch.cuda.Stream] = None):
-        """One step; the step number goes up by one. `factors` as in adamw_step."""
+        """One step; the step numbers of the parameters that have a gradient go up by one. `factors` as in
+        adamw_step, for parameters that share a step number; a captured step needs them, and every captured step has to
+        update the same parameters."""
         who = [i for i, p in enumerate(self.params) if p.grad is not None]
-
-        def of(ts):
-            return [ts[i] for i in who]
-        adamw_step(of(self.params), [self.params[i].grad for i in who], of(self.exp_avg), of(self.exp_avg_sq),
-                   self.steps + 1, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, of(self.master),
-                   None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors, stream=stream)
-        self.steps += 1
+        if not who:
+            return
+        device = self.params[0].device
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the parameters on {device}")
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+            counts = self._counts if capturing else self.counts()
+            groups = {}
+            for i in who:
+                groups.setdefault(counts[i], []).append(i)
+            if factors is not None and len(groups) > 1:
+                raise ValueError(f"factors are of one step number, the parameters are at {sorted(groups)}")
+            if capturing and factors is None:
+                raise ValueError("a captured step needs factors: without them each replay would repeat one step number")
+            if capturing and self._captured not in (None, who):
+                raise ValueError("another captured step updates other parameters: load this state into a new AdamW for that")
+            grads = [p.grad for p in self.params]
+            if len(groups) > 1:     # all gradients are checked before the first group's step
+                _like("grads", [grads[i] for i in who], [self.params[i].numel() for i in who], self.params[0].get_device(), _WEIGHTS)
+            if capturing:
+                self._replays.add_(1)
+            for count, group in groups.items():
+                def of(ts):
+                    return [ts[i] for i in group]
+                # with factors the number that 8-bit states round by is read on the device: the host's steps and the replays
+                number = self._counts[group[0]] + (0 if capturing else 1) if factors is not None else count + 1
+                _adamw(of(self.params), of(grads), of(self.exp_avg), of(self.exp_avg_sq), number, self.lr, self.betas, self.eps,
+                       self.weight_decay, grad_scale, of(self.master),
+                       None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors,
+                       self._replays if factors is not None else None)
+            if capturing:
+                self._captured = who
+            else:
+                for i in who:
+                    self._counts[i] += 1
 
     def state_dict(self) -> dict:
-        """States and step number, for a checkpoint (tensors are the live ones)."""
-        return {"steps": self.steps, "state_bits": self.state_bits, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
-                "scales": self.scales, "master": self.master}
+        """States and step numbers, for a checkpoint (tensors are the live ones)."""
+        counts = self.counts()
+        return {"steps": max(counts, default=0), "counts": counts, "state_bits": self.state_bits, "exp_avg": self.exp_avg,
+                "exp_avg_sq": self.exp_avg_sq, "scales": self.scales, "master": self.master}
 
     def load_state_dict(self, state: dict):
-        """Copies a state_dict of the same parameters and state_bits back in."""
+        """Copies a state_dict of the same parameters and state_bits back in. One without "counts" has "steps" for all."""
         if state["state_bits"] != self.state_bits or len(state["exp_avg"]) != len(self.params):
             raise ValueError("the state is of other parameters or another state_bits")
+        counts = list(state.get("counts") or [state["steps"]] * len(self.params))
+        if len(counts) != len(self.params):
+            raise ValueError("the state is of other parameters")
         with torch.no_grad():
             for mine, theirs in ((self.exp_avg, state["exp_avg"]), (self.exp_avg_sq, state["exp_avg_sq"]),
                                  (self.master, state["master"])):
@@ -490,4 +545,5 @@ class AdamW:
                 for mine, theirs in zip(self.scales, state["scales"]):
                     for a, b in zip(mine, theirs):
                         a.copy_(b)
-        self.steps = state["steps"]
+        replayed = [a - b for a, b in zip(self.counts(), self._counts)]
+        self._counts = [c - r for c, r in zip(counts, replayed)]
