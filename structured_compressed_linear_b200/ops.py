@@ -75,6 +75,11 @@ def _streamed(fn):
     return call
 
 
+def _written(*tensors):
+    """Tells autograd that `tensors` were changed in place: a backward pass that saved one of them refuses to run on it."""
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _apart(out: torch.Tensor, name: str, **inputs):
     """A given output must not share memory with an input."""
     a, b = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
@@ -129,6 +134,8 @@ def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bi
     mean, rstd = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
     _call(device, lib().ss1_layernorm_forward, X.data_ptr(), _ptr(weight),
           _ptr(bias), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), M, K, eps, _dtype_code(X.dtype), _dtype_code(wt))
+    if out is not None:
+        _written(out)
     return Y, mean, rstd
 
 
@@ -254,7 +261,8 @@ def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.
     `out` may be Y itself. keep: returns (out, H) with H = X A^T, float32 [M, R], for the backward pass."""
     device, M, K, N, R, ad, code, n = _adapters(X, A, B, index, scale, plan)
     _tensor("Y", Y, (M, N), X.dtype, device)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty_like(Y)
     else:
         _tensor("out", out, Y.shape, Y.dtype, device)
@@ -265,6 +273,8 @@ def adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, Y: torch.
     ws = X.new_empty(size, dtype=torch.uint8)
     _call(device, L.ss1_adapter_forward, ad, X.data_ptr(), Y.data_ptr(), out.data_ptr(), _ptr(H), M,
           ws.data_ptr(), size)
+    if given:
+        _written(out)
     return (out, H) if keep else out
 
 
@@ -423,6 +433,7 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
         raise ValueError("device_step goes with factors, and 8-bit states with factors need it")
     hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
     _call(device, lib().ss1_adamw_step_ex, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), _ptr(device_step))
+    _written(*params, *exp_avg, *exp_avg_sq, *(t for t in master or () if t is not None), *(t for part in scales or () for t in part))
 
 
 class AdamW:
