@@ -18,6 +18,7 @@ from typing import List, Optional, Sequence, Tuple
 
 import numpy as np
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ss1
 from .ss1 import _check, _dtype_code, lib
@@ -175,6 +176,7 @@ class LayerNormFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, mean, rstd, weight = ctx.saved_tensors
         dX, dw, db = layernorm_backward(dY.contiguous(), X, mean, rstd, weight, tuple(ctx.needs_input_grad[:3]))
@@ -319,6 +321,7 @@ class AdaptedSS1Function(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, Wc, A, B, H, index, scale = ctx.saved_tensors
         dY = dY.contiguous()

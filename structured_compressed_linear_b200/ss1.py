@@ -15,6 +15,7 @@ from typing import Optional, Tuple
 
 import numpy as np
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libss1.so")
@@ -445,6 +446,7 @@ class SS1Function(torch.autograd.Function):
         return layer.forward(X.contiguous(), Wc.contiguous())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, Wc = ctx.saved_tensors
         dY = dY.contiguous()

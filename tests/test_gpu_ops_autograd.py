@@ -74,3 +74,21 @@ def test_a_backward_pass_that_saved_out_is_refused(libs):
         ops.adapter_forward(x, a, b, z, out=z)
     with pytest.raises(RuntimeError, match="inplace|in-place|modified"):
         loss.backward()
+
+
+def test_second_derivatives_are_refused(libs):
+    """create_graph=True is fine for a first derivative; a second one through the operators is an error, not a missing term."""
+    ss1, ops = libs
+    M, K, N, R = 40, 256, 128, 8
+    x, w, b, Wc, A, B = _leaves((M, K), (K,), (K,), (N, K // 2), (1, R, K), (1, N, R))
+    layer = ss1.SS1Layer(K, N, 2, 128, 128, 3)
+    for make, leaf in ((lambda: ops.LayerNormFunction.apply(x, w, b, 1e-5), w),
+                       (lambda: ops.AdaptedSS1Function.apply(x, Wc, layer, A, B), A),
+                       (lambda: ss1.SS1Function.apply(x, Wc, layer), Wc)):
+        y = make()
+        plain, = torch.autograd.grad(y.square().sum(), leaf)
+        first, = torch.autograd.grad(make().square().sum(), leaf, create_graph=True)
+        assert torch.equal(plain, first.detach())
+        with pytest.raises(RuntimeError, match="once_differentiable|differentiat"):
+            first.square().sum().backward()
+    layer.close()
