@@ -309,7 +309,8 @@ def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torc
 
 class AdaptedSS1Function(torch.autograd.Function):
     """Autograd wrapper of an SS1 layer with low-rank adapters beside it:
-    Y = AdaptedSS1Function.apply(X, Wc, layer, A, B, index, scale, plan), the last three as in adapter_forward."""
+    Y = AdaptedSS1Function.apply(X, Wc, layer, A, B, index, scale, plan), the last three as in adapter_forward. `scale` has
+    no gradient: the backward pass refuses one that asks for it."""
 
     @staticmethod
     def forward(ctx, X, Wc, layer, A, B, index=None, scale=None, plan=None):
@@ -323,6 +324,8 @@ class AdaptedSS1Function(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
+        if any(ctx.needs_input_grad[6:7]):
+            raise ValueError("scale has no gradient here: pass scale.detach()")
         X, Wc, A, B, H, index, scale = ctx.saved_tensors
         dY = dY.contiguous()
         nx, nw, _, na, nb = ctx.needs_input_grad[:5]

@@ -92,3 +92,18 @@ def test_second_derivatives_are_refused(libs):
         with pytest.raises(RuntimeError, match="once_differentiable|differentiat"):
             first.square().sum().backward()
     layer.close()
+
+
+def test_scale_has_no_gradient(libs):
+    ss1, ops = libs
+    x, Wc, A, B, scale = _leaves((8, 256), (128, 128), (1, 8, 256), (1, 128, 8), (1,))
+    layer = ss1.SS1Layer(256, 128, 2, 128, 128, 3)
+    with torch.no_grad():
+        y = ops.AdaptedSS1Function.apply(x, Wc, layer, A, B, None, scale)
+    z = ops.AdaptedSS1Function.apply(x, Wc, layer, A, B, None, scale)
+    assert torch.equal(y, z)
+    with pytest.raises(ValueError, match="scale"):
+        z.sum().backward()
+    ops.AdaptedSS1Function.apply(x, Wc, layer, A, B, None, scale.detach()).sum().backward()
+    assert A.grad is not None and scale.grad is None
+    layer.close()
