@@ -142,16 +142,21 @@ def layernorm_forward(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bi
 
 @_streamed
 def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
-                       weight: Optional[torch.Tensor] = None, need: Tuple[bool, bool, bool] = (True, True, True)):
+                       weight: Optional[torch.Tensor] = None, need: Tuple[bool, bool, bool] = (True, True, True),
+                       weight_dtype: Optional[torch.dtype] = None):
     """(dX, dweight, dbias) from dY, the forward's X, mean and rstd (ss1_layernorm_backward). dweight and
-    dbias have weight's dtype (X's without a weight). `need`: which of the three to compute (the
-    others are None)."""
+    dbias have weight's dtype; without a weight weight_dtype (X's or float32: the bias's), or X's. `need`: which of the
+    three to compute (the others are None)."""
     M, K = _norm_rows(X)
     device = X.get_device()
     _tensor("dY", dY, X.shape, X.dtype, device)
     _tensor("mean", mean, X.shape[:1], torch.float32, device)
     _tensor("rstd", rstd, X.shape[:1], torch.float32, device)
     wt = _norm_weights(X, device, weight)
+    if weight_dtype is not None and weight_dtype != wt:
+        if weight is not None or weight_dtype != torch.float32:
+            raise ValueError(f"weight_dtype must be {wt}" + ("" if weight is not None else " or torch.float32"))
+        wt = weight_dtype
     L = lib()
     dX = torch.empty_like(X) if need[0] else None
     dw = X.new_empty(K, dtype=wt) if need[1] else None
@@ -179,10 +184,8 @@ class LayerNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY):
         X, mean, rstd, weight = ctx.saved_tensors
-        dX, dw, db = layernorm_backward(dY.contiguous(), X, mean, rstd, weight, tuple(ctx.needs_input_grad[:3]))
-        if db is not None and db.dtype != ctx.bias_dtype:   # a float32 bias without a weight beside bf16 rows
-            db = db.to(ctx.bias_dtype)
-        return dX, dw, db, None
+        # a bias without a weight may be float32 beside bf16 rows
+        return *layernorm_backward(dY.contiguous(), X, mean, rstd, weight, tuple(ctx.needs_input_grad[:3]), ctx.bias_dtype), None
 
 
 # ---- low-rank adapters -----------------------------------------------------------------------
