@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import struct
 from operator import attrgetter
 from typing import List, Optional, Sequence, Tuple
@@ -64,15 +65,18 @@ def _call(device: int, fn, *args):
 def _streamed(fn):
     """Adds the argument `stream`: the call, and what it allocates, then belong to that stream. (Memory that another
     stream's allocator handed out could still be in use there.)"""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
+    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
         if stream is None:
-            return fn(first, *args, **kw)
-        t = first[0] if isinstance(first, (list, tuple)) and first else first
+            return fn(*args, **kw)
+        t = args[0] if args else kw.get(name)
+        t = t[0] if isinstance(t, (list, tuple)) and t else t
         if isinstance(t, torch.Tensor) and t.device != stream.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
