@@ -116,7 +116,7 @@ def _norm_rows(X: torch.Tensor) -> Tuple[int, int]:
     return X.shape
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _norm_workspace(L, M: int, K: int) -> int:
     n = ctypes.c_size_t()
     _check(L.ss1_layernorm_backward_workspace(M, K, ctypes.byref(n)), "ss1_layernorm_backward_workspace")
@@ -205,7 +205,7 @@ class AdapterPlan:
         self.data, self.M, self.count = data, M, count
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _plan_bytes(L, M: int, count: int) -> int:
     n = ctypes.c_size_t()
     _check(L.ss1_adapter_plan_bytes(M, count, ctypes.byref(n)), "ss1_adapter_plan_bytes")

@@ -38,3 +38,14 @@ def test_every_argument_by_name(ops):
         with pytest.raises(TypeError):
             fn(**dict(list(kw.items())[1:]))     # the first one is missing
     ops.adamw_step(params=[], grads=[], exp_avg=[], exp_avg_sq=[])
+
+
+def test_size_caches_are_bounded(ops):
+    """Ragged batches have ever new sizes; what is remembered of them stays bounded."""
+    from structured_compressed_linear_b200 import ss1
+    L = ss1.load_library()
+    for cached, args in ((ops._norm_workspace, (64,)), (ops._plan_bytes, (3,))):
+        for M in range(1, 5000):
+            cached(L, M, *args)
+        assert cached.cache_info().currsize <= 4096
+    assert ops._adapter_workspace.cache_parameters()["maxsize"] == 4096
