@@ -552,22 +552,23 @@ class AdamW:
 
     def load_state_dict(self, state: dict):
         """Copies a state_dict of the same parameters and state_bits back in. One without "counts" has "steps" for all."""
-        if state["state_bits"] != self.state_bits or len(state["exp_avg"]) != len(self.params):
-            raise ValueError("the state is of other parameters or another state_bits")
+        if state["state_bits"] != self.state_bits:
+            raise ValueError(f"the state has {state['state_bits']} bits, this optimizer {self.state_bits}")
         counts = list(state.get("counts") or [state["steps"]] * len(self.params))
         if len(counts) != len(self.params):
             raise ValueError("the state is of other parameters")
+        pairs = [(name, getattr(self, name), state[name]) for name in ("exp_avg", "exp_avg_sq", "master")]
+        if self.scales is not None:
+            pairs += [("scales", mine, theirs) for mine, theirs in zip(self.scales, state["scales"] or ((), ()))]
+        for name, mine, theirs in pairs:       # everything is checked before anything is written
+            if len(mine) != len(theirs) or any((a is None) != (b is None) for a, b in zip(mine, theirs)):
+                raise ValueError(f"{name}: the state is of other parameters or master copies")
+            if any(a is not None and (a.shape != b.shape or a.dtype != b.dtype) for a, b in zip(mine, theirs)):
+                raise ValueError(f"{name}: a tensor of the state has another shape or type")
         with torch.no_grad():
-            for mine, theirs in ((self.exp_avg, state["exp_avg"]), (self.exp_avg_sq, state["exp_avg_sq"]),
-                                 (self.master, state["master"])):
+            for _, mine, theirs in pairs:
                 for a, b in zip(mine, theirs):
-                    if (a is None) != (b is None):
-                        raise ValueError("master copies: one side has one, the other none")
                     if a is not None:
-                        a.copy_(b)
-            if self.scales is not None:
-                for mine, theirs in zip(self.scales, state["scales"]):
-                    for a, b in zip(mine, theirs):
                         a.copy_(b)
         replayed = [a - b for a, b in zip(self.counts(), self._counts)]
         self._counts = [c - r for c, r in zip(counts, replayed)]

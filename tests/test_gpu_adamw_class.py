@@ -171,3 +171,34 @@ def test_refusals(ops):
     old = {k: v for k, v in opt.state_dict().items() if k != "counts"}
     opt.load_state_dict(dict(old, steps=7))
     assert opt.counts() == [7, 7] and opt.steps == 7
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_of_other_parameters_changes_nothing(ops, bits):
+    """States whose tensors would only broadcast, or that are short of some, are refused before anything is copied."""
+    def make(sizes, master=True):
+        ps = [torch.ones(n, dtype=BF16, device="cuda", requires_grad=True) for n in sizes]
+        opt = ops.AdamW(ps, state_bits=bits, master=master)
+        for p in ps:
+            p.grad = torch.ones_like(p)
+        opt.step()
+        return opt
+
+    def tensors(opt):
+        return [t.clone() for part in (opt.exp_avg, opt.exp_avg_sq, opt.master, *(opt.scales or ())) for t in part]
+    mine, good = make((600, 300)), make((600, 300)).state_dict()
+    before = tensors(mine)
+    bad = [make((600, 1)).state_dict(), make((600, 300), master=False).state_dict(), dict(good, exp_avg_sq=good["exp_avg_sq"][:1]),
+           dict(good, master=good["master"][:1]), dict(good, exp_avg_sq=[t.double() for t in good["exp_avg_sq"]]),
+           dict(good, state_bits=40 - bits), dict(good, counts=[3])]
+    if bits == 8:
+        bad += [dict(good, scales=(good["scales"][0], good["scales"][1][:1])), dict(good, scales=None),
+                dict(good, scales=(good["scales"][0], [t[:1] for t in good["scales"][1]]))]
+    for i, state in enumerate(bad):
+        for x in (state["exp_avg"][0], state["exp_avg_sq"][0]):
+            x.add_(1)                              # what a partial load would bring in
+        with pytest.raises(ValueError):
+            mine.load_state_dict(state)
+        assert all(torch.equal(a, b) for a, b in zip(before, tensors(mine))), i
+        assert mine.counts() == [1, 1]
+    mine.load_state_dict(good)
