@@ -397,7 +397,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     root of the second one), float32 [ceil(numel / ADAMW_BLOCK)] each, uint8 E4M3 codes instead. `step` numbers
     the parameters' steps from 1 on: past ADAMW_NEAREST, codes are rounded up or down by a hash of it.
     master: float32 copies of bf16 params, which the step then reads and writes (None: has none). factors: float32
-    CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale. device_step: int64 CUDA tensor [1],
+    CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale. No tensor that is written may overlap
+    another one of the call. device_step: int64 CUDA tensor [1],
     the step's number beside `factors`, read on the device too; 8-bit states with factors need it."""
     _adamw(params, grads, exp_avg, exp_avg_sq, 0 if device_step is not None else step, lr, betas, eps, weight_decay, grad_scale,
            master, scales, factors, device_step)
@@ -415,13 +416,12 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
     sizes = list(map(_NUMEL, params))
     table = np.zeros(n, _ADAMW_TENSOR)
     where = _like("params", params, sizes, device, _WEIGHTS)
-    if len(set(where)) < n and len({p for p, size in zip(where, sizes) if size}) < sum(size > 0 for size in sizes):
-        raise ValueError("a parameter is in the list twice")
     table["param"] = where
     table["grad"] = _like("grads", grads, sizes, device, _WEIGHTS)
     state = _F32 if bits == 32 else _U8
-    table["exp_avg"] = _like("exp_avg", exp_avg, sizes, device, state)
-    table["exp_avg_sq"] = _like("exp_avg_sq", exp_avg_sq, sizes, device, state)
+    table["exp_avg"] = avg = _like("exp_avg", exp_avg, sizes, device, state)
+    table["exp_avg_sq"] = sq = _like("exp_avg_sq", exp_avg_sq, sizes, device, state)
+    written = [*where, *avg, *sq]
     table["numel"] = sizes
     for field, ts in (("param_dtype", params), ("grad_dtype", grads)):
         kinds = set(map(_DTYPE, ts))
@@ -430,14 +430,19 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
         if len(master) != n:
             raise ValueError(f"master: {len(master)} tensors for {n} parameters")
         some = [i for i, t in enumerate(master) if t is not None]
-        if len(some) == n:
-            table["master"] = _like("master", master, sizes, device, _F32)
-        elif some:
-            table["master"][some] = _like("master", [master[i] for i in some], [sizes[i] for i in some], device, _F32)
+        if some:
+            at = _like("master", [master[i] for i in some], [sizes[i] for i in some], device, _F32)
+            table["master"][slice(None) if len(some) == n else some] = at
+            written += at
     if scales is not None:
         blocks = [-(-size // ADAMW_BLOCK) for size in sizes]
-        table["avg_scale"] = _like("scales[0]", scales[0], blocks, device, _F32)
-        table["sq_scale"] = _like("scales[1]", scales[1], blocks, device, _F32)
+        table["avg_scale"] = avg = _like("scales[0]", scales[0], blocks, device, _F32)
+        table["sq_scale"] = sq = _like("scales[1]", scales[1], blocks, device, _F32)
+        written += avg + sq
+    if len(set(written)) < len(written):
+        full = [p for p in written if p]               # empty tensors have no address
+        if len(set(full)) < len(full):
+            raise ValueError("a tensor is given twice: parameters, moments, scales and master copies are written at the same time")
     if factors is not None:
         _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
     if device_step is not None:

@@ -202,3 +202,24 @@ def test_a_state_of_other_parameters_changes_nothing(ops, bits):
         assert all(torch.equal(a, b) for a, b in zip(before, tensors(mine))), i
         assert mine.counts() == [1, 1]
     mine.load_state_dict(good)
+
+
+def test_a_tensor_given_twice_is_refused(ops):
+    """Whatever is written may be given once only, whichever list it is in; gradients may be shared; empty tensors have no address."""
+    def new(k, dt=F32):
+        return [torch.zeros(300, dtype=dt, device="cuda") for _ in range(k)]
+    P, (g,), M, V, W = new(2, BF16), new(1, BF16), new(2), new(2), new(2)
+    eight, sc = new(4, torch.uint8), [torch.zeros(2, device="cuda") for _ in range(4)]
+    G = [g, g]
+    for bad in (lambda: ops.adamw_step(P, G, M, M), lambda: ops.adamw_step(P, G, [M[0], M[0]], V), lambda: ops.adamw_step(P, G, M, [V[0], M[0]]),
+                lambda: ops.adamw_step(P, G, M, V, master=[W[0], W[0]]), lambda: ops.adamw_step(P, G, M, V, master=[None, M[1]]),
+                lambda: ops.adamw_step(P[:1], G[:1], M[:1], V[:1], master=V[:1]),
+                lambda: ops.adamw_step(P, G, eight[:2], eight[2:], scales=(sc[:2], sc[:2])),
+                lambda: ops.adamw_step(P, G, eight[:2], eight[:2], scales=(sc[:2], sc[2:]))):
+        with pytest.raises(ValueError, match="twice"):
+            bad()
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in (*P, *M, *V, *W, *eight, *sc))
+    empty = [torch.zeros(0, device="cuda") for _ in range(3)]
+    ops.adamw_step(empty, empty, empty, empty)
+    ops.adamw_step([*P, empty[0]], [*G, empty[0]], [*M, empty[0]], [*V, empty[0]], master=[W[0], None, None])
