@@ -917,7 +917,8 @@ constexpr int second_smem() {
 template <int RT>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_kernel(const Columns da, int na, const Update dx,
                                                                                       PlanView plan, int M, int R, int n) {
-    // CTAs of both launches may share an SM: their tensor memory has room, or shared memory for one of them only
+    // CTAs of both launches may share an SM: their tensor memory has room, or shared memory for one of them only. (The decode
+    // kernel, which holds tensor memory while it waits, takes 166 KB of shared memory or more: never beside one of these.)
     static_assert(RT <= 64 ? 2 * ColumnsShape<RT>::columns <= 512 && first_smem<RT>() + 2 * second_smem<RT>() > 232448
                            : first_smem<RT>() + second_smem<RT>() > 232448, "512 columns an SM");
     extern __shared__ uint8_t raw[];
