@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const Prepare d, Plan
 // ragged rows (34 MB, 5.1 us at the copy rate), the plan's time hidden in part by bring_ahead. H (TRANS false) is handed out in float32, so each stage's MMAs start from zero and are
 // added in registers: the tensor core's own accumulation truncates, over thousands of columns by more than
 // float32's rounding. G (TRANS true) only feeds bf16 results: tcgen05 multiplies out of the ring as it lies
-// there and accumulates in tensor memory, one thread issuing four instructions a stage.
-constexpr int kStages = 4;
+// there and accumulates in tensor memory, one thread issuing four instructions a stage. Those sums are taken out into
+// registers and begun again every 4096 columns: over all of 131,072 columns of one sign they came out 8e-4 too small.
+constexpr int kStages = 4, kTakeStages = 64;
 
 template <int RT, bool TRANS>
 struct ProductsShape {
@@ -344,44 +345,65 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
     float* part = reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw)));   // later, over the ring's memory
     if (TRANS) {
         constexpr uint32_t kColumns = RT < 32 ? 32 : RT, kInstr = idesc_mn(RT, false, true);
+        // A warp's lanes are 32 of the tile's rows; warps 4 - 7 take the upper half of the ranks, where that is 16 or more.
+        constexpr int kHalf = RT < 32 ? RT : RT / 2;
+        const bool reads = RT >= 32 || warp < 4;
+        const int row = warp % 4 * 32 + lane, j0 = warp / 4 * kHalf;
+        float sum[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
         tensor_begin(ts, kColumns);
         const uint32_t tmem = ts.tmem;
+        // adds what tensor memory holds, after the wait for its last product
+        auto take = [&] {
+            ptx::tc_fence_after();
+            if (!reads) return;
+#pragma unroll
+            for (int j = 0; j < kHalf; j += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(warp % 4 * 32) << 16) + j0 + j, v);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_fence_regs<16>(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(v[i]);
+            }
+            ptx::tc_fence_before();
+        };
+        bool fresh = true;
         for (int chunk = from, slot = 0; chunk < to; ++chunk, slot = slot + 1 == kStages ? 0 : slot + 1) {
             ptx::cp_async_wait<kStages - 2>();
             ptx::fence_proxy_async_smem();
             __syncthreads();
             if (tid == 0) {
                 const uint32_t su = base + slot * S::stage, stt = su + S::u_bytes;
+                ptx::tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    ptx::umma_bf16_ss(tmem, desc_k(su + k * 32), desc_mn(stt + k * 2048, 8192), kInstr, chunk > from || k > 0);
+                    ptx::umma_bf16_ss(tmem, desc_k(su + k * 32), desc_mn(stt + k * 2048, 8192), kInstr, !fresh || k > 0);
                 ptx::umma_commit(&ts.done[slot]);
             }
+            fresh = false;
             const int last = slot == 0 ? kStages - 1 : slot - 1;      // the slot of the stage before: loaded again once read
             if (chunk > from) tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1);
             load(chunk + kStages - 1 < to, last);
+            if ((chunk + 1 - from) % kTakeStages == 0 && chunk + 1 < to) {
+                tensor_wait(ts, slot, ((chunk - from) / kStages) & 1);
+                take();
+                fresh = true;      // the barrier above comes before the next product overwrites what was read
+            }
         }
-        if (to > from) tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1);
+        if (to > from) {
+            tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1);
+            take();
+        }
         ptx::cp_async_wait<0>();
-        ptx::tc_fence_after();
         __syncthreads();
         const bool valid = *(volatile int*)&ts.gave_up == 0;
-        if (warp < 4) {                                               // lane = row of the tile
+        if (reads) {
+            float4* to_row = reinterpret_cast<float4*>(part + row * S::pitch + j0);
 #pragma unroll
-            for (int j = 0; j < RT; j += 16) {
-                uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(tmem + ((uint32_t)(warp * 32) << 16) + j, v);
-                ptx::tmem_ld_wait();
-                ptx::tmem_ld_fence_regs<16>(v);
-                float4* to_row = reinterpret_cast<float4*>(part + tid * S::pitch + j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = to > from ? (valid ? __uint_as_float(v[4 * i + k]) : NAN) : 0.0f;
-                    to_row[i] = make_float4(x[0], x[1], x[2], x[3]);
-                }
-            }
+            for (int j = 0; j < kHalf; j += 4)
+                to_row[j / 4] = valid ? make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]) : make_float4(NAN, NAN, NAN, NAN);
         }
         tensor_end(ts, kColumns);
     } else {
@@ -1001,6 +1023,7 @@ int stage_splits(int64_t C, int tiles, int ctas, int most) {
 
 // CTAs of each part of the backward's two launches
 constexpr int kFirstCtas = 148, kColumnsCtas = 148, kUpdateCtas = 296;
+constexpr int kRunTiles = 32;      // of a run in dA or dB, about
 
 // H packed and A transposed where the pointers are given, B widened where R is no multiple of 8; *B and *ld: B as
 // the kernels read it.
@@ -1118,9 +1141,15 @@ int mma_rank(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)
 int mma_runs(int64_t M, int64_t C, int n) {
     // one CTA an SM for each gradient, since both launches do other work beside (two: 8192 x 768 x 2304, rank 32, 57 us
     // instead of 48), and a run for every tile while they are few (two tiles a run: 2048 x 768 x 2304 37 us instead of 29)
-    int64_t s = kColumnsCtas / ((C + kColCols - 1) / kColCols);
-    const int64_t most = M / kTile + n;
+    const int64_t ranges = (C + kColCols - 1) / kColCols, tiles = M / kTile;
+    int64_t s = kColumnsCtas / ranges;
+    const int64_t most = tiles + n;
     s = s > most ? most : s;
+    // Tensor memory truncates its sums: 9 runs of 524,288 rows of one sign came out 3e-4 too small, as much as
+    // bf16 rounds by. So a run has about 32 tiles at most (4096 rows: 1e-5), within what the grid can count.
+    int64_t least = (tiles + (n < tiles ? n : tiles) + kRunTiles - 1) / kRunTiles;
+    if (least > 32000 / ranges) least = 32000 / ranges;
+    s = s < least ? least : s;
     return (int)(s < 1 ? 1 : s);
 }
 
