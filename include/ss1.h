@@ -440,7 +440,7 @@ SS1_API int ss1_test_bounds_check(int64_t index, int64_t extent);
  * there where the formula has an infinity. The kernels are launched with programmatic dependent
  * launch: they may start while the previous kernel on the stream is running, but read and write
  * nothing before it is over, so stream order holds as for any launch. Tensor-core kernels bound their
- * waits (2 s); one that ran out would leave NaN in what it computes.
+ * waits (2 s); one that runs out leaves NaN in what it computes and reports to ss1_adapter_status.
  */
 
 /*
@@ -543,6 +543,27 @@ SS1_API int ss1_adapter_forward(const ss1_adapters* adapters, const void* X, con
 SS1_API int ss1_adapter_backward(const ss1_adapters* adapters, const void* dY, const void* X, const float* H,
                                  const void* dX_in, void* dX, void* dA, void* dB, int64_t M, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * ss1_adapter_status -- reads and clears the current device's word of bounded waits that ran out in
+ * ss1_adapter_backward. Call after synchronising the streams whose work is to be looked at. Returns SS1_OK or
+ * SS1_ERR_DEVICE_TIMEOUT; *detail (may be NULL) receives the raw code of the first one: (4 << 8) | 0x80 |
+ * site, with site 1 for G, 2 for dB, 3 for dA. Not for use while a stream is being captured. Errors: CUDA.
+ */
+SS1_API int ss1_adapter_status(int32_t* detail);
+
+/*
+ * ss1_test_adapter_timeout -- exercises the time-out path of ss1_adapter_backward without a fault, for tests of
+ * failure handling. Runs it (bf16 sizes that its tensor-core kernels take, all three gradients asked for) with
+ * every wait cut to limit_ns nanoseconds (1 .. 2e9), while the first CTA of `site` (1 G of the first 128 rows,
+ * 2 dB, 3 dA) does not announce the products of its first stage. Its wait runs out, it writes the status word,
+ * issues and waits for nothing more, lets what it issued end, frees its tensor memory and leaves NaN: site 1 in the
+ * first rows of dX and in dA of their adapters, 2 in dB, 3 in dA. Asynchronous. Errors: as
+ * ss1_adapter_backward; INVALID_ARG (site, limit_ns), UNSUPPORTED_SHAPE (not the tensor-core kernels').
+ */
+SS1_API int ss1_test_adapter_timeout(const ss1_adapters* adapters, const void* dY, const void* X, const float* H,
+                                     const void* dX_in, void* dX, void* dA, void* dB, int64_t M, void* workspace,
+                                     size_t workspace_bytes, int site, int64_t limit_ns, void* stream);
 
 /*
  * AdamW (Loshchilov & Hutter, "Decoupled Weight Decay Regularization"), one step over many tensors:

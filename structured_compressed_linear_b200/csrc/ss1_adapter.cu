@@ -801,9 +801,9 @@ extern "C" SS1_API int ss1_adapter_forward(const ss1_adapters* ad, const void* X
     return SS1_OK;
 }
 
-extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* dY, const void* X, const float* H, const void* dX_in,
-                                            void* dX, void* dA, void* dB, int64_t M, void* workspace, size_t workspace_bytes,
-                                            void* stream) {
+// `test`: the time-out test, on the tensor-core path or not at all.
+static int adapter_backward(const ss1_adapters* ad, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA,
+                            void* dB, int64_t M, void* workspace, size_t workspace_bytes, const Watch* test, void* stream) {
     const int rc = check(ad, M);
     if (rc != SS1_OK) return rc;
     const size_t e = dtype_size(ad->dtype);
@@ -824,9 +824,10 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
     if (!workspace || workspace_bytes < s.backward()) return SS1_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     Call c = call_of(*ad, M);
+    const bool mma = mma_shape(*ad, M) && aligned(dY, 16) && aligned(X, 16) && aligned(dX_in, 16) && aligned(dX, 16);
+    if (test && !mma) return SS1_ERR_UNSUPPORTED_SHAPE;
     err = plan_of(*ad, M, ws, c, st);
-    if (err == cudaSuccess && mma_shape(*ad, M) && aligned(dY, 16) && aligned(X, 16) && aligned(dX_in, 16) &&
-        aligned(dX, 16)) {
+    if (err == cudaSuccess && mma) {
         uint8_t* at = ws + s.plan;
         MmaSpace w;
         w.packed_g = at; at += s.packed;
@@ -835,7 +836,7 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
         w.turned_a = at; at += s.turned_a;
         w.part_a = reinterpret_cast<float*>(at); at += s.part_a;
         w.part_b = reinterpret_cast<float*>(at);
-        err = mma_backward(c, dY, X, H, dX_in, dX, dA, dB, w, st);
+        err = mma_backward(c, dY, X, H, dX_in, dX, dA, dB, w, test, st);
         if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
         return SS1_OK;
     }
@@ -847,4 +848,26 @@ extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* 
                                           : backward_general<float>(c, dY, X, H, dX_in, dX, dA, dB, G, part_a, part_b, st);
     if (err != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
     return SS1_OK;
+}
+
+extern "C" SS1_API int ss1_adapter_backward(const ss1_adapters* ad, const void* dY, const void* X, const float* H, const void* dX_in,
+                                            void* dX, void* dA, void* dB, int64_t M, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+    return adapter_backward(ad, dY, X, H, dX_in, dX, dA, dB, M, workspace, workspace_bytes, nullptr, stream);
+}
+
+extern "C" SS1_API int ss1_test_adapter_timeout(const ss1_adapters* ad, const void* dY, const void* X, const float* H, const void* dX_in,
+                                                void* dX, void* dA, void* dB, int64_t M, void* workspace, size_t workspace_bytes,
+                                                int site, int64_t limit_ns, void* stream) {
+    if (site < kTimeoutG || site > kTimeoutDa || limit_ns < 1 || limit_ns > 2000000000 || M < 1 || !dX || !dA || !dB)
+        return SS1_ERR_INVALID_ARG;
+    const Watch watch{(uint64_t)limit_ns, site};
+    return adapter_backward(ad, dY, X, H, dX_in, dX, dA, dB, M, workspace, workspace_bytes, &watch, stream);
+}
+
+extern "C" SS1_API int ss1_adapter_status(int32_t* detail) {
+    int32_t v = 0;
+    if (mma_status(&v) != cudaSuccess) { cudaGetLastError(); return SS1_ERR_CUDA; }
+    if (detail) *detail = v;
+    return v == 0 ? SS1_OK : SS1_ERR_DEVICE_TIMEOUT;
 }

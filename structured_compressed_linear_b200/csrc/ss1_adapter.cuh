@@ -53,8 +53,17 @@ struct MmaSpace {
 int mma_rank(int R);                             // R as the kernels pad it
 int mma_runs(int64_t M, int64_t C, int n);       // runs of tiles in dA or dB with C columns
 cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, float* H, const MmaSpace& w, cudaStream_t st);
+// The test of a wait that runs out: waits end after limit_ns, and the first CTA at `withhold` (a TimeoutSite) does not announce
+// the products of its first stage.
+struct Watch {
+    uint64_t limit_ns;
+    int withhold;
+};
+enum TimeoutSite : int { kTimeoutG = 1, kTimeoutDb, kTimeoutDa };     // with the kernel id 4 in the status word
+constexpr int32_t kStatusKernelAdapter = 4;
 cudaError_t mma_backward(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
-                         const MmaSpace& w, cudaStream_t st);
+                         const MmaSpace& w, const Watch* test, cudaStream_t st);
+cudaError_t mma_status(int32_t* detail);         // reads and clears the current device's status word
 
 }  // namespace ada
 }  // namespace ss1

@@ -71,19 +71,27 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t next) { return
 // The same kind of box with the rows along M or N.
 __device__ __forceinline__ uint64_t desc_k(uint32_t at) { return ptx::smem_desc(at, 16, 1024, ptx::kLayoutSW128); }
 
-// The tensor core's part of a CTA: one completion barrier a ring slot, and what says that a wait gave up (after two
-// seconds, where the products of a stage take a microsecond). Then nothing is waited for any more and
-// the CTA's results are NaN.
+// How waits are bounded: two seconds, where the products of a stage take a microsecond. A test's kernels (others, so
+// that these pay nothing for it: 2 %) take a Watch in its place.
+struct Unwatched {
+    static constexpr uint64_t limit_ns = 2000000000ull;
+    static constexpr int withhold = 0;
+};
+
+// The tensor core's part of a CTA: one completion barrier a ring slot, and what says that a wait gave up. Then nothing
+// is multiplied or waited for any more, the status word is set, what was issued ends before its memory is freed
+// (or a second limit does), and the CTA's results are NaN.
 constexpr int kSlots = 6;
+__device__ int32_t g_status;      // the first time-out since it was read: kernel id << 8 | 0x80 | site
 struct TensorState {
-    uint64_t done[kSlots];
+    uint64_t done[kSlots];        // the last one: for the end after a wait gave up
     uint32_t tmem;
-    int gave_up;
+    int gave_up, never;           // never: 0
 };
 __device__ __forceinline__ void tensor_begin(TensorState& t, uint32_t columns) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) ptx::mbar_init(&t.done[i], 1);
-        t.gave_up = 0;
+        t.gave_up = t.never = 0;
         ptx::fence_mbar_init();
     }
     if (threadIdx.x < 32) {
@@ -94,14 +102,28 @@ __device__ __forceinline__ void tensor_begin(TensorState& t, uint32_t columns) {
     __syncthreads();
     ptx::tc_fence_after();
 }
-__device__ __forceinline__ void tensor_wait(TensorState& t, int slot, uint32_t parity) {
-    if (!ptx::mbar_wait(&t.done[slot], parity, &t.gave_up, 2000000000ull)) *(volatile int*)&t.gave_up = 1;
+__device__ __forceinline__ bool tensor_fine(const TensorState& t) { return *(const volatile int*)&t.gave_up == 0; }
+// False, and the CTA's waits end, where this wait or another one gave up.
+template <typename W>
+__device__ __forceinline__ bool tensor_wait(TensorState& t, int slot, uint32_t parity, const W& watch) {
+    if (ptx::mbar_wait(&t.done[slot], parity, &t.gave_up, watch.limit_ns)) return true;
+    *(volatile int*)&t.gave_up = 1;
+    return false;
 }
 // All threads, after the last wait and the last read of tensor memory.
-__device__ __forceinline__ void tensor_end(TensorState& t, uint32_t columns) {
+template <typename W>
+__device__ __forceinline__ void tensor_end(TensorState& t, uint32_t columns, const W& watch, int site) {
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    if (!tensor_fine(t)) {
+        if (threadIdx.x == 0) {
+            atomicCAS(&g_status, 0, (kStatusKernelAdapter << 8) | 0x80 | site);
+            ptx::umma_commit(&t.done[kSlots - 1]);
+            ptx::mbar_wait(&t.done[kSlots - 1], 0, &t.never, watch.limit_ns);
+        }
+        __syncthreads();
+    }
     if (threadIdx.x < 32) ptx::tmem_dealloc(t.tmem, columns);
 }
 
@@ -258,9 +280,9 @@ struct Products {
     bool table_is_new;
 };
 
-template <int RT, bool TRANS>
+template <int RT, bool TRANS, typename W>
 __device__ __forceinline__ void products_role(const Products& d, const PlanView& plan, int tile_index, uint8_t* raw, TensorState& ts, int M,
-                                              int R, int n) {
+                                              int R, int n, const W& watch) {
     using S = ProductsShape<RT, TRANS>;
     const bf16 *U = d.U, *table = d.table;
     const float* scale = d.scale;
@@ -354,6 +376,7 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
         for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
         tensor_begin(ts, kColumns);
         const uint32_t tmem = ts.tmem;
+        const bool withhold = watch.withhold == kTimeoutG && tile_index == 0 && split == 0;
         // adds what tensor memory holds, after the wait for its last product
         auto take = [&] {
             ptx::tc_fence_after();
@@ -369,43 +392,43 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
             }
             ptx::tc_fence_before();
         };
-        bool fresh = true;
+        bool fresh = true, fine = true;     // fine: none of this thread's waits gave up
         for (int chunk = from, slot = 0; chunk < to; ++chunk, slot = slot + 1 == kStages ? 0 : slot + 1) {
             ptx::cp_async_wait<kStages - 2>();
             ptx::fence_proxy_async_smem();
             __syncthreads();
-            if (tid == 0) {
+            if (tid == 0 && fine) {
                 const uint32_t su = base + slot * S::stage, stt = su + S::u_bytes;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     ptx::umma_bf16_ss(tmem, desc_k(su + k * 32), desc_mn(stt + k * 2048, 8192), kInstr, !fresh || k > 0);
-                ptx::umma_commit(&ts.done[slot]);
+                if (!withhold || chunk > from) ptx::umma_commit(&ts.done[slot]);
             }
             fresh = false;
             const int last = slot == 0 ? kStages - 1 : slot - 1;      // the slot of the stage before: loaded again once read
-            if (chunk > from) tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1);
+            if (chunk > from) fine &= tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1, watch);
             load(chunk + kStages - 1 < to, last);
             if ((chunk + 1 - from) % kTakeStages == 0 && chunk + 1 < to) {
-                tensor_wait(ts, slot, ((chunk - from) / kStages) & 1);
+                fine &= tensor_wait(ts, slot, ((chunk - from) / kStages) & 1, watch);
                 take();
                 fresh = true;      // the barrier above comes before the next product overwrites what was read
             }
         }
         if (to > from) {
-            tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1);
+            tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1, watch);
             take();
         }
         ptx::cp_async_wait<0>();
         __syncthreads();
-        const bool valid = *(volatile int*)&ts.gave_up == 0;
+        const bool valid = tensor_fine(ts);
         if (reads) {
             float4* to_row = reinterpret_cast<float4*>(part + row * S::pitch + j0);
 #pragma unroll
             for (int j = 0; j < kHalf; j += 4)
                 to_row[j / 4] = valid ? make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]) : make_float4(NAN, NAN, NAN, NAN);
         }
-        tensor_end(ts, kColumns);
+        tensor_end(ts, kColumns, watch, kTimeoutG);
     } else {
         float sum[RT / 8][4];
 #pragma unroll
@@ -496,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) products_kernel(const Products d, co
     bring_ahead(ahead, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
     wait_for_previous();
     let_next_start();      // update_kernel reads Y and B before its own wait: they are complete here
-    products_role<RT, false>(d, plan, blockIdx.y, raw, unused, M, R, n);
+    products_role<RT, false>(d, plan, blockIdx.y, raw, unused, M, R, n, Unwatched());
 }
 
 // ---- update ----------------------------------------------------------------------------------
@@ -744,11 +767,11 @@ __device__ __forceinline__ int tiles_a_run(const PlanView& plan, int n, int M, i
     return max(1, (tiles + runs - 1) / runs);
 }
 
-template <int RT>
+template <int RT, typename W>
 __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& plan, int range, int run, uint8_t* raw, TensorState& ts,
-                                             int M, int R, int n, bool packed_is_new) {
+                                             int M, int R, int n, bool packed_is_new, const W& watch, int site) {
     using S = ColumnsShape<RT>;
-    static_assert(S::stages <= kSlots, "a barrier a slot");
+    static_assert(S::stages < kSlots, "a barrier a slot, and one for the end");
     const uint32_t base = (ptx::smem_u32(raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int C = d.C, c0 = range * kColCols;
@@ -822,17 +845,18 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
     for (int s = 0; s < S::stages - 1; ++s) advance(s);
     tensor_begin(ts, S::columns);
     const uint32_t tmem = ts.tmem;
+    const bool withhold = watch.withhold == site && range == 0 && run == 0;
     constexpr uint32_t kInstr = idesc_mn(2 * RT, true, true);
     const int64_t size = (int64_t)C * R;
-    bool fresh = true;
+    bool fresh = true, fine = true;        // fine: none of this thread's waits gave up
     for (int step = 0, slot = 0;; ++step) {
         if (step % kColSteps == 0 || step == steps) {       // a tile begins, or the run ends
             const int a = step < steps ? next_adapter : -1;
             if (step + kColSteps < steps) next_adapter = tile_of(plan, t0 + step / kColSteps + 1, M).adapter;
             if (a != adapter && (unsigned)adapter < (unsigned)n) {
-                tensor_wait(ts, slot == 0 ? S::stages - 1 : slot - 1, ((step - 1) / S::stages) & 1);
+                fine &= tensor_wait(ts, slot == 0 ? S::stages - 1 : slot - 1, ((step - 1) / S::stages) & 1, watch);
                 ptx::tc_fence_after();
-                const bool valid = *(volatile int*)&ts.gave_up == 0;
+                const bool valid = tensor_fine(ts);
                 const int2 own = adapter_tiles(plan, adapter, M);
                 const bool whole = own.x >= t0 && own.y <= t1;
                 const int64_t place = whole ? adapter * size : (int64_t)(run + adapter) * size;
@@ -884,7 +908,7 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
         ptx::cp_async_wait<S::stages - 2>();
         ptx::fence_proxy_async_smem();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && fine) {
             const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
             ptx::tc_fence_after();
 #pragma unroll
@@ -893,18 +917,18 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
                 for (int h = 0; h < 2; ++h)
                     ptx::umma_bf16_ss(tmem + h * 2 * RT, desc_mn(su + h * 2 * S::box + k * 2048, S::box), desc_mn(sp + k * 2048, S::box), kInstr,
                                       !fresh || k > 0);
-            ptx::umma_commit(&ts.done[slot]);
+            if (!withhold || step > 0) ptx::umma_commit(&ts.done[slot]);
         }
         fresh = false;
         const int last = slot == 0 ? S::stages - 1 : slot - 1;        // the slot of the step before: loaded again once read
-        if (step > 0) tensor_wait(ts, last, ((step - 1) / S::stages) & 1);
+        if (step > 0) fine &= tensor_wait(ts, last, ((step - 1) / S::stages) & 1, watch);
         load_u(step + S::stages - 1, last);
         load_p(now, step + S::stages - 1, last);
         advance(step + S::stages - 1);
         slot = slot == S::stages - 1 ? 0 : slot + 1;
     }
     ptx::cp_async_wait<0>();
-    tensor_end(ts, S::columns);
+    tensor_end(ts, S::columns, watch, site);
 }
 
 // G and dB in one launch: both read dY (from HBM once: the other reader finds it in L2). The first `tiles` rows of
@@ -914,18 +938,19 @@ constexpr int first_smem() {
     return ColumnsShape<RT>::smem > ProductsShape<RT, true>::smem ? ColumnsShape<RT>::smem : ProductsShape<RT, true>::smem;
 }
 
-template <int RT>
+template <int RT, typename W>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) first_gradients_kernel(const Products g, int tiles, const Columns db, int nb,
-                                                                                     PlanView plan, int M, int R, int n) {
+                                                                                     PlanView plan, int M, int R, int n,
+                                                                                     const W watch) {
     extern __shared__ uint8_t raw[];
     __shared__ TensorState ts;
     if ((int)blockIdx.y < tiles) {
-        products_role<RT, true>(g, plan, blockIdx.y, raw, ts, M, R, n);
+        products_role<RT, true>(g, plan, blockIdx.y, raw, ts, M, R, n, watch);
     } else {
         wait_for_previous();      // the packed H
         let_next_start();
         const int k = ((int)blockIdx.y - tiles) * gridDim.x + blockIdx.x, ranges = (db.C + kColCols - 1) / kColCols;
-        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, ts, M, R, n, false);
+        if (k < nb) columns_role<RT>(db, plan, k % ranges, k / ranges, raw, ts, M, R, n, false, watch, kTimeoutDb);
     }
 }
 
@@ -936,9 +961,10 @@ constexpr int second_smem() {
     return ColumnsShape<RT>::smem > UpdateShape<RT>::smem ? ColumnsShape<RT>::smem : UpdateShape<RT>::smem;
 }
 
-template <int RT>
+template <int RT, typename W>
 __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_kernel(const Columns da, int na, const Update dx,
-                                                                                      PlanView plan, int M, int R, int n) {
+                                                                                      PlanView plan, int M, int R, int n,
+                                                                                      const W watch) {
     // CTAs of both launches may share an SM: their tensor memory has room, or shared memory for one of them only. (The decode
     // kernel, which holds tensor memory while it waits, takes 166 KB of shared memory or more: never beside one of these.)
     static_assert(RT <= 64 ? 2 * ColumnsShape<RT>::columns <= 512 && first_smem<RT>() + 2 * second_smem<RT>() > 232448
@@ -949,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 64 ? 2 : 1) second_gradients_k
     const int i = blockIdx.x;
     if (i < na) {
         const int ranges = (da.C + kColCols - 1) / kColCols;
-        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, ts, M, R, n, true);
+        columns_role<RT>(da, plan, i % ranges, i / ranges, raw, ts, M, R, n, true, watch, kTimeoutDa);
     } else {
         update_role<RT>(dx, plan, tile_of(plan, (i - na) / dx.splits, M), (i - na) % dx.splits, raw, M, R, n);
     }
@@ -1095,11 +1121,11 @@ cudaError_t forward_rt(const Call& c, const void* X, const void* Y, void* out, f
     return launch_dependent(ufn, dim3((unsigned)usplits, (unsigned)tiles), dim3(kThreads), SU::smem, st, d, c.plan, (int)c.M, c.R, c.n);
 }
 
-template <int RT>
+template <int RT, typename W>
 cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
-                        const MmaSpace& w, cudaStream_t st) {
-    auto* fn1 = &first_gradients_kernel<RT>;
-    auto* fn2 = &second_gradients_kernel<RT>;
+                        const MmaSpace& w, const W& watch, cudaStream_t st) {
+    auto* fn1 = &first_gradients_kernel<RT, W>;
+    auto* fn2 = &second_gradients_kernel<RT, W>;
     int ld;
     const void* B;
     bool prepared;
@@ -1116,13 +1142,13 @@ cudaError_t backward_rt(const Call& c, const void* dY, const void* X, const floa
     const int splits = stage_splits(c.N, tiles, kFirstCtas, kPortableCluster);
     const Products g{(const bf16*)dY, (const bf16*)B, c.scale, nullptr, (bf16*)w.packed_g, (int)c.N, ld, B != c.B};
     e = launch_clusters(fn1, dim3((unsigned)splits, (unsigned)(gtiles + (nb + splits - 1) / splits)), splits, first_smem<RT>(), prepared, st,
-                        g, gtiles, db, nb, c.plan, (int)c.M, c.R, c.n);
+                        g, gtiles, db, nb, c.plan, (int)c.M, c.R, c.n, watch);
     if (e != cudaSuccess) return e;
     if (dX || dA) {
         const Update dx{(const bf16*)w.packed_g, (const bf16*)w.turned_a, (const bf16*)dX_in, (bf16*)dX, (int)c.K, ld,
                         stage_splits(c.K, tiles, kUpdateCtas, 1 << 20)};
         const int64_t ctas = (int64_t)na + (dX ? (int64_t)tiles * dx.splits : 0);
-        e = launch_dependent(fn2, dim3((unsigned)ctas), dim3(kThreads), second_smem<RT>(), st, da, na, dx, c.plan, (int)c.M, c.R, c.n);
+        e = launch_dependent(fn2, dim3((unsigned)ctas), dim3(kThreads), second_smem<RT>(), st, da, na, dx, c.plan, (int)c.M, c.R, c.n, watch);
         if (e != cudaSuccess) return e;
     }
     if (!dA && !dB) return cudaSuccess;
@@ -1162,14 +1188,31 @@ cudaError_t mma_forward(const Call& c, const void* X, const void* Y, void* out, 
     }
 }
 
-cudaError_t mma_backward(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
-                         const MmaSpace& w, cudaStream_t st) {
+namespace {
+template <typename W>
+cudaError_t backward_of(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
+                        const MmaSpace& w, const W& watch, cudaStream_t st) {
     switch (mma_rank(c.R)) {
-        case 16: return backward_rt<16>(c, dY, X, H, dX_in, dX, dA, dB, w, st);
-        case 32: return backward_rt<32>(c, dY, X, H, dX_in, dX, dA, dB, w, st);
-        case 64: return backward_rt<64>(c, dY, X, H, dX_in, dX, dA, dB, w, st);
-        default: return backward_rt<128>(c, dY, X, H, dX_in, dX, dA, dB, w, st);
+        case 16: return backward_rt<16>(c, dY, X, H, dX_in, dX, dA, dB, w, watch, st);
+        case 32: return backward_rt<32>(c, dY, X, H, dX_in, dX, dA, dB, w, watch, st);
+        case 64: return backward_rt<64>(c, dY, X, H, dX_in, dX, dA, dB, w, watch, st);
+        default: return backward_rt<128>(c, dY, X, H, dX_in, dX, dA, dB, w, watch, st);
     }
+}
+}  // namespace
+
+cudaError_t mma_backward(const Call& c, const void* dY, const void* X, const float* H, const void* dX_in, void* dX, void* dA, void* dB,
+                         const MmaSpace& w, const Watch* test, cudaStream_t st) {
+    return test ? backward_of(c, dY, X, H, dX_in, dX, dA, dB, w, *test, st) : backward_of(c, dY, X, H, dX_in, dX, dA, dB, w, Unwatched(), st);
+}
+
+cudaError_t mma_status(int32_t* detail) {
+    int32_t v = 0;
+    const int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof v);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_status, &zero, sizeof zero);
+    if (e == cudaSuccess) *detail = v;
+    return e;
 }
 
 }  // namespace ada

@@ -314,6 +314,15 @@ def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torc
     return out, dA, dB
 
 
+def adapter_status(device: Optional[int] = None) -> Tuple[int, int]:
+    """(status, detail) of `device` (the current one): whether a bounded wait of adapter_backward ran out since the last look
+    (ss1_adapter_status; its results are NaN then). Call after synchronising."""
+    detail = ctypes.c_int32()
+    with torch.cuda.device(device):
+        status = lib().ss1_adapter_status(ctypes.byref(detail))
+    return status, detail.value
+
+
 class AdaptedSS1Function(torch.autograd.Function):
     """Autograd wrapper of an SS1 layer with low-rank adapters beside it:
     Y = AdaptedSS1Function.apply(X, Wc, layer, A, B, index, scale, plan), the last three as in adapter_forward. `scale` has

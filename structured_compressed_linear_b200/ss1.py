@@ -29,7 +29,7 @@ SYMBOLS = ("ss1_create", "ss1_forward", "ss1_forward_with", "ss1_select_kernel",
            "ss1_chain_fused", "ss1_test_forward_timeout", "ss1_last_launch", "ss1_bounds_check",
            "ss1_test_bounds_check", "ss1_layernorm_forward", "ss1_layernorm_backward_workspace",
            "ss1_layernorm_backward", "ss1_adapter_plan_bytes", "ss1_adapter_plan", "ss1_adapter_workspace",
-           "ss1_adapter_forward", "ss1_adapter_backward", "ss1_adamw_step", "ss1_adamw_step_ex", "ss1_adamw_factors")
+           "ss1_adapter_forward", "ss1_adapter_backward", "ss1_adapter_status", "ss1_test_adapter_timeout", "ss1_adamw_step", "ss1_adamw_step_ex", "ss1_adamw_factors")
 
 #: (N / BN) * K limit of ss1_forward_noalloc (SS1_NOALLOC_MAX_ENTRIES in include/ss1.h).
 NOALLOC_MAX_ENTRIES = 983040
@@ -112,6 +112,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ss1_adapter_workspace.argtypes = [i64, i64, i64, i32, i32, i32, pz, pz]
     L.ss1_adapter_forward.argtypes = [vp, vp, vp, vp, vp, i64, vp, sz, vp]
     L.ss1_adapter_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    L.ss1_adapter_status.argtypes = [vp]
+    L.ss1_test_adapter_timeout.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, sz, i32, i64, vp]
     L.ss1_adamw_step.argtypes = [vp, i64, i32, vp, vp, vp]
     L.ss1_adamw_step_ex.argtypes = [vp, i64, i32, vp, vp, vp, vp]
     L.ss1_adamw_factors.argtypes = [vp, vp]
