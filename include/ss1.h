@@ -77,7 +77,8 @@ enum ss1_status {
     SS1_ERR_MISALIGNED = -5,         /* a pointer is not 16-byte aligned                      */
     SS1_ERR_DEVICE_TIMEOUT = -6,     /* a kernel gave up a bounded wait (see ss1_device_status)*/
     SS1_ERR_BAD_HANDLE = -7,         /* null or destroyed handle                              */
-    SS1_ERR_UNSUPPORTED_SHAPE = -8   /* this kernel cannot run this shape (choose another)    */
+    SS1_ERR_UNSUPPORTED_SHAPE = -8,  /* this kernel cannot run this shape (choose another)    */
+    SS1_ERR_OVERLAP = -9             /* memory that a call writes overlaps other memory of it */
 };
 
 /*
@@ -604,8 +605,9 @@ typedef struct {
 
 /*
  * ss1_adamw_step -- one step over `count` tensors.
- *   tensors : host array, read during the call. Tensors must not overlap one another. numel == 0
- *             is allowed (pointers unused).
+ *   tensors : host array, read during the call. What is written (parameters, master copies, moments, scales) must not
+ *             overlap anything else of the call, but a gradient may be its own parameter's memory in the same
+ *             type. Gradients may be shared. numel == 0 is allowed (pointers unused).
  *   state_bits : 32 or 8, for all tensors. All-zero bytes are a valid start in both.
  *   hyper   : host; unused where device_factors is given (but see device_step).
  *   device_factors : NULL, or device float [SS1_ADAMW_FACTORS] as ss1_adamw_factors writes them, read
@@ -614,7 +616,7 @@ typedef struct {
  * call has changed nothing. Asynchronous. Errors: INVALID_ARG (sizes, types, NULL pointers, a master
  * copy beside float32 parameters, hyper-parameters out of range: 0 <= beta < 1, eps >= 0, step >= 1,
  * finite; 8-bit states with device_factors, which need ss1_adamw_step_ex), MISALIGNED (a pointer not
- * aligned to its element), CUDA.
+ * aligned to its element), OVERLAP, OUT_OF_MEMORY (of the host), CUDA.
  */
 SS1_API int ss1_adamw_step(const ss1_adamw_tensor* tensors, int64_t count, int state_bits, const ss1_adamw_hyper* hyper,
                            const float* device_factors, void* stream);

@@ -35,6 +35,9 @@
 #include <cuda_fp8.h>
 
 #include <math.h>
+#include <stdlib.h>
+
+#include <algorithm>
 
 namespace ss1 {
 namespace {
@@ -382,6 +385,42 @@ Factors factors(const ss1_adamw_hyper& h) {
     return f;
 }
 
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+};
+
+// Whether something that the step writes overlaps anything else of it: the CTAs of all tensors run at once. `r`: 7 places a tensor.
+bool overlaps(const ss1_adamw_tensor* tensors, int64_t count, int bits, Range* r) {
+    Range* end = r;
+    auto add = [&end](const void* p, int64_t n, size_t size, bool written) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (p) *end++ = Range{lo, lo + (uintptr_t)n * size, written};
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const ss1_adamw_tensor& t = tensors[i];
+        if (t.numel == 0) continue;
+        const size_t state = bits == 32 ? 4 : 1;
+        add(t.param, t.numel, dtype_size(t.param_dtype), true);
+        if (t.grad != t.param || t.grad_dtype != t.param_dtype) add(t.grad, t.numel, dtype_size(t.grad_dtype), false);
+        add(t.master, t.numel, 4, true);
+        add(t.exp_avg, t.numel, state, true);
+        add(t.exp_avg_sq, t.numel, state, true);
+        if (bits == 8) {
+            add(t.avg_scale, (t.numel + kBlock - 1) / kBlock, 4, true);
+            add(t.sq_scale, (t.numel + kBlock - 1) / kBlock, 4, true);
+        }
+    }
+    std::sort(r, end, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;      // ends of what lies before
+    for (; r < end; ++r) {
+        if (r->lo < written || (r->written && r->lo < any)) return true;
+        any = std::max(any, r->hi);
+        if (r->written) written = std::max(written, r->hi);
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace ss1
 
@@ -424,6 +463,11 @@ extern "C" SS1_API int ss1_adamw_step_ex(const ss1_adamw_tensor* tensors, int64_
             (state_bits == 8 && (!aligned(t.avg_scale, 4) || !aligned(t.sq_scale, 4))))
             return SS1_ERR_MISALIGNED;
     }
+    Range* const ranges = static_cast<Range*>(malloc((size_t)count * 7 * sizeof(Range) + 1));
+    if (!ranges) return SS1_ERR_OUT_OF_MEMORY;
+    const bool bad = overlaps(tensors, count, state_bits, ranges);
+    free(ranges);
+    if (bad) return SS1_ERR_OVERLAP;
     Factors f = {};
     if (!device_factors) f = factors(*hyper);
     const int64_t step = hyper ? hyper->step : 0;

@@ -240,6 +240,7 @@ SS1_API const char* ss1_strerror(int status) {
         case SS1_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait (device status set)";
         case SS1_ERR_BAD_HANDLE: return "bad or destroyed handle";
         case SS1_ERR_UNSUPPORTED_SHAPE: return "the chosen kernel does not support this shape";
+        case SS1_ERR_OVERLAP: return "memory that the call writes overlaps other memory of it";
         default: return "unknown status";
     }
 }

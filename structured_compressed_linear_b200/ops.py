@@ -10,6 +10,7 @@ is alive (autograd ties a leaf to the stream of its first use).
 
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import inspect
@@ -80,7 +81,7 @@ def _streamed(fn):
     return call
 
 
-def _written(*tensors):
+def _written(tensors):
     """Tells autograd that `tensors` were changed in place: a backward pass that saved one of them refuses to run on it."""
     torch.autograd.graph.increment_version(tensors)
 
@@ -382,13 +383,14 @@ _POINTER, _NUMEL, _CONTIGUOUS, _DEVICE = (torch.Tensor.data_ptr, torch.Tensor.nu
 _DTYPE = attrgetter("dtype")
 
 
-def _like(name: str, ts: Sequence[torch.Tensor], sizes: List[int], device: int, dtypes) -> List[int]:
-    """The tensors' addresses, after the checks."""
+def _like(name: str, ts: Sequence[torch.Tensor], sizes: List[int], device: int, dtypes):
+    """(the tensors' addresses, their types), after the checks."""
     if list(map(_NUMEL, ts)) != sizes:
         raise ValueError(f"{name}: one tensor for each parameter, of its size")
-    if set(map(_DEVICE, ts)) - {device} or not all(map(_CONTIGUOUS, ts)) or not set(map(_DTYPE, ts)) <= dtypes:
+    kinds = set(map(_DTYPE, ts))
+    if set(map(_DEVICE, ts)) - {device} or not all(map(_CONTIGUOUS, ts)) or not kinds <= dtypes:
         raise ValueError(f"{name} must be contiguous, on cuda:{device} and of " + " or ".join(map(str, dtypes)))
-    return list(map(_POINTER, ts))
+    return array.array("Q", map(_POINTER, ts)), kinds
 
 
 _WEIGHTS, _F32, _U8 = {torch.bfloat16, torch.float32}, {torch.float32}, {torch.uint8}
@@ -407,7 +409,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], ex
     the parameters' steps from 1 on: past ADAMW_NEAREST, codes are rounded up or down by a hash of it.
     master: float32 copies of bf16 params, which the step then reads and writes (None: has none). factors: float32
     CUDA tensor of adamw_factors, read on the device in place of step .. grad_scale. No tensor that is written may overlap
-    another one of the call. device_step: int64 CUDA tensor [1],
+    another one of the call (but a gradient may be its parameter itself). device_step: int64 CUDA tensor [1],
     the step's number beside `factors`, read on the device too; 8-bit states with factors need it."""
     _adamw(params, grads, exp_avg, exp_avg_sq, 0 if device_step is not None else step, lr, betas, eps, weight_decay, grad_scale,
            master, scales, factors, device_step)
@@ -424,34 +426,32 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
     bits = 32 if scales is None else 8
     sizes = list(map(_NUMEL, params))
     table = np.zeros(n, _ADAMW_TENSOR)
-    where = _like("params", params, sizes, device, _WEIGHTS)
-    table["param"] = where
-    table["grad"] = _like("grads", grads, sizes, device, _WEIGHTS)
     state = _F32 if bits == 32 else _U8
-    table["exp_avg"] = avg = _like("exp_avg", exp_avg, sizes, device, state)
-    table["exp_avg_sq"] = sq = _like("exp_avg_sq", exp_avg_sq, sizes, device, state)
-    written = [*where, *avg, *sq]
+    changed = [*params, *exp_avg, *exp_avg_sq]
+    table["param"], pt = _like("params", params, sizes, device, _WEIGHTS)
+    table["grad"], gt = _like("grads", grads, sizes, device, _WEIGHTS)
+    table["exp_avg"], _ = _like("exp_avg", exp_avg, sizes, device, state)
+    table["exp_avg_sq"], _ = _like("exp_avg_sq", exp_avg_sq, sizes, device, state)
+    table["param_dtype"] = _dtype_code(pt.pop()) if len(pt) == 1 else [_dtype_code(t.dtype) for t in params]
+    table["grad_dtype"] = _dtype_code(gt.pop()) if len(gt) == 1 else [_dtype_code(t.dtype) for t in grads]
     table["numel"] = sizes
-    for field, ts in (("param_dtype", params), ("grad_dtype", grads)):
-        kinds = set(map(_DTYPE, ts))
-        table[field] = _dtype_code(kinds.pop()) if len(kinds) == 1 else [_dtype_code(t.dtype) for t in ts]
     if master is not None:
         if len(master) != n:
             raise ValueError(f"master: {len(master)} tensors for {n} parameters")
-        some = [i for i, t in enumerate(master) if t is not None]
-        if some:
-            at = _like("master", [master[i] for i in some], [sizes[i] for i in some], device, _F32)
-            table["master"][slice(None) if len(some) == n else some] = at
-            written += at
+        if all(map(torch.is_tensor, master)):
+            table["master"], _ = _like("master", master, sizes, device, _F32)
+            changed += master
+        else:
+            some = [i for i, t in enumerate(master) if t is not None]
+            if some:
+                mine = [master[i] for i in some]
+                table["master"][some], _ = _like("master", mine, [sizes[i] for i in some], device, _F32)
+                changed += mine
     if scales is not None:
         blocks = [-(-size // ADAMW_BLOCK) for size in sizes]
-        table["avg_scale"] = avg = _like("scales[0]", scales[0], blocks, device, _F32)
-        table["sq_scale"] = sq = _like("scales[1]", scales[1], blocks, device, _F32)
-        written += avg + sq
-    if len(set(written)) < len(written):
-        full = [p for p in written if p]               # empty tensors have no address
-        if len(set(full)) < len(full):
-            raise ValueError("a tensor is given twice: parameters, moments, scales and master copies are written at the same time")
+        for k, name in enumerate(("avg_scale", "sq_scale")):
+            table[name], _ = _like(f"scales[{k}]", scales[k], blocks, device, _F32)
+            changed += scales[k]
     if factors is not None:
         _tensor("factors", factors, (ADAMW_FACTORS,), torch.float32, device)
     if device_step is not None:
@@ -459,8 +459,14 @@ def _adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_deca
     if (device_step is not None) > (factors is not None) or (bits == 8 and factors is not None and device_step is None):
         raise ValueError("device_step goes with factors, and 8-bit states with factors need it")
     hyper = _AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step)
-    _call(device, lib().ss1_adamw_step_ex, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), _ptr(device_step))
-    _written(*params, *exp_avg, *exp_avg_sq, *(t for t in master or () if t is not None), *(t for part in scales or () for t in part))
+    try:
+        _call(device, lib().ss1_adamw_step_ex, table.ctypes.data, n, bits, ctypes.byref(hyper), _ptr(factors), _ptr(device_step))
+    except ss1.SS1Error as e:
+        if e.status == -9:
+            raise ValueError("a tensor is given twice, or overlaps another: parameters, moments, scales and master copies are "
+                             "written at the same time") from None
+        raise
+    _written(changed)
 
 
 class AdamW:
@@ -526,37 +532,47 @@ class AdamW:
         device = self.params[0].device
         if stream is not None and stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the parameters on {device}")
-        with torch.cuda.device(device), torch.cuda.stream(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-            counts = self._counts if capturing else self.counts()
+        if stream is not None or torch.cuda.current_device() != device.index:
+            with torch.cuda.device(device), torch.cuda.stream(stream):
+                self._step(who, grad_scale, factors)
+        else:
+            self._step(who, grad_scale, factors)
+
+    def _step(self, who: List[int], grad_scale: float, factors: Optional[torch.Tensor]):
+        """step on the current device and stream, of the parameters `who`."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        counts = self._counts if capturing or self._captured is None else self.counts()
+        grads = [p.grad for p in self.params]
+        if len({counts[i] for i in who}) == 1:
+            groups = {counts[who[0]]: who}
+        else:
             groups = {}
             for i in who:
                 groups.setdefault(counts[i], []).append(i)
-            if factors is not None and len(groups) > 1:
+            if factors is not None:
                 raise ValueError(f"factors are of one step number, the parameters are at {sorted(groups)}")
-            if capturing and factors is None:
+            # all gradients are checked before the first group's step
+            _like("grads", [grads[i] for i in who], [self.params[i].numel() for i in who], self.params[0].get_device(), _WEIGHTS)
+        if capturing:
+            if factors is None:
                 raise ValueError("a captured step needs factors: without them each replay would repeat one step number")
-            if capturing and self._captured not in (None, who):
+            if self._captured not in (None, who):
                 raise ValueError("another captured step updates other parameters: load this state into a new AdamW for that")
-            grads = [p.grad for p in self.params]
-            if len(groups) > 1:     # all gradients are checked before the first group's step
-                _like("grads", [grads[i] for i in who], [self.params[i].numel() for i in who], self.params[0].get_device(), _WEIGHTS)
-            if capturing:
-                self._replays.add_(1)
-            for count, group in groups.items():
-                def of(ts):
-                    return [ts[i] for i in group]
-                # with factors the number that 8-bit states round by is read on the device: the host's steps and the replays
-                number = self._counts[group[0]] + (0 if capturing else 1) if factors is not None else count + 1
-                _adamw(of(self.params), of(grads), of(self.exp_avg), of(self.exp_avg_sq), number, self.lr, self.betas, self.eps,
-                       self.weight_decay, grad_scale, of(self.master),
-                       None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors,
-                       self._replays if factors is not None else None)
-            if capturing:
-                self._captured = who
-            else:
-                for i in who:
-                    self._counts[i] += 1
+            self._replays.add_(1)
+        for count, group in groups.items():
+            def of(ts):
+                return ts if len(group) == len(ts) else [ts[i] for i in group]
+            # with factors the number that 8-bit states round by is read on the device: the host's steps and the replays
+            number = self._counts[group[0]] + (0 if capturing else 1) if factors is not None else count + 1
+            _adamw(of(self.params), of(grads), of(self.exp_avg), of(self.exp_avg_sq), number, self.lr, self.betas, self.eps,
+                   self.weight_decay, grad_scale, of(self.master),
+                   None if self.scales is None else (of(self.scales[0]), of(self.scales[1])), factors,
+                   self._replays if factors is not None else None)
+        if capturing:
+            self._captured = who
+        else:
+            for i in who:
+                self._counts[i] += 1
 
     def state_dict(self) -> dict:
         """States and step numbers, for a checkpoint (tensors are the live ones)."""

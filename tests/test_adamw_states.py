@@ -118,3 +118,44 @@ def test_refusals():
     assert call(8, None, None, h=None) == -1
     text = open(os.path.join(ROOT, "include", "ss1.h")).read()
     assert int(re.search(r"#define\s+SS1_ADAMW_NEAREST\s+(\d+)", text).group(1)) == ops.ADAMW_NEAREST == S.NEAREST
+
+
+def test_overlaps():
+    """Memory that a step writes may not overlap anything else of it (made-up addresses; refused before a device is touched)."""
+    from structured_compressed_linear_b200 import build, ops, ss1
+    import ctypes
+    build.build()
+    lib = ss1.load_library()
+    hyper = ops._AdamWHyper(1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0, 1)
+    OVERLAP, K = -9, 1 << 20
+    assert lib.ss1_strerror(OVERLAP) != lib.ss1_strerror(12345)
+
+    def call(bits, *rows, factors=None):
+        t = np.zeros(len(rows), ops._ADAMW_TENSOR)
+        for i, row in enumerate(rows):
+            t[i] = (*(K * a + b for a, b in row[:7]), 1000, *row[7:])
+        return lib.ss1_adamw_step_ex(t.ctypes.data, len(rows), bits, ctypes.byref(hyper), factors, None, None)
+
+    def entry(first, **change):
+        """Param, grad, master, moments and scales at megabytes first, first + 1, ..., bf16."""
+        names = ("param", "grad", "master", "exp_avg", "exp_avg_sq", "avg_scale", "sq_scale")
+        at = {k: (first + i, 0) for i, k in enumerate(names)}
+        at.update(change)
+        return (*(at[k] for k in names), 0, 0)
+    a, none = entry(1), (0, 0)
+    for bits, size in ((32, 4), (8, 1)):
+        for k, n in (("param", 2000), ("grad", 2000), ("master", 4000), ("exp_avg", 1000 * size), ("exp_avg_sq", 1000 * size)):
+            for other, m in (("param", 2000), ("exp_avg", 1000 * size), ("exp_avg_sq", 1000 * size)):
+                if other == k:
+                    continue
+                at = dict(zip(("param", "grad", "master", "exp_avg", "exp_avg_sq"), a))[other]
+                # on it, its last bytes, and from below into its first ones (a gradient on its parameter is allowed)
+                shifts = [4 * ((m - 1) // 4), -4 * ((n - 1) // 4)] + ([0] if (k, other) != ("grad", "param") else [])
+                for shift in shifts:
+                    assert call(bits, entry(1, **{k: (at[0], shift)})) == OVERLAP, (bits, k, other, shift)
+        assert call(bits, a, entry(20, param=(1, 0))) == OVERLAP and call(bits, a, entry(20, grad=(1, 0))) == OVERLAP
+        assert call(bits, entry(20, param=(2, 0)), a) == OVERLAP          # another entry's gradient
+        assert call(bits, a, entry(20, exp_avg=(4, 4 * ((1000 * size - 1) // 4)))) == OVERLAP
+        assert call(bits, entry(20), a, entry(40, master=(23, 0))) == OVERLAP
+    assert call(8, entry(1, sq_scale=(6, 0))) == OVERLAP and call(8, a, entry(20, avg_scale=(6, 12))) == OVERLAP
+    assert call(8, entry(1, master=none, avg_scale=(4, 996))) == OVERLAP

@@ -223,3 +223,10 @@ def test_a_tensor_given_twice_is_refused(ops):
     empty = [torch.zeros(0, device="cuda") for _ in range(3)]
     ops.adamw_step(empty, empty, empty, empty)
     ops.adamw_step([*P, empty[0]], [*G, empty[0]], [*M, empty[0]], [*V, empty[0]], master=[W[0], None, None])
+    flat = torch.zeros(1000, device="cuda")        # neighbours touch, but do not overlap; a gradient that is its parameter
+    ops.adamw_step([flat[:100]], [flat[:100]], [flat[100:200]], [flat[200:300]])
+    ops.adamw_step([flat[:100], flat[300:400]], [flat[800:900], flat[850:950]], [flat[100:200], flat[400:500]], [flat[200:300], flat[500:600]])
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.adamw_step([flat[:100]], [flat[300:400]], [flat[99:199]], [flat[200:300]])
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.adamw_step([flat[:100]], [flat[50:150]], [flat[400:500]], [flat[200:300]])
