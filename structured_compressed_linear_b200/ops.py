@@ -512,6 +512,7 @@ class AdamW:
         """Each parameter's number of steps. Waits for the device once a step was captured."""
         if self._captured is None:
             return list(self._counts)
+        torch.cuda.synchronize(self._replays.device)       # a replay may run on any stream
         replays, captured = int(self._replays), set(self._captured)
         return [c + replays if i in captured else c for i, c in enumerate(self._counts)]
 

@@ -126,6 +126,23 @@ def test_replays_are_counted(ops, bits):
         assert torch.equal(a, b)
 
 
+def test_replays_on_another_stream_are_counted(ops):
+    """A replay that waits behind other work on a stream of its own is part of the count."""
+    p = torch.zeros(64, device="cuda", requires_grad=True)
+    p.grad = torch.ones(64, device="cuda")
+    opt = ops.AdamW([p], lr=LR)
+    factors = ops.adamw_factors(1, LR).cuda()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        opt.step(factors=factors)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)              # about ten milliseconds
+        graph.replay()
+    assert opt.steps == 1
+    torch.cuda.synchronize()
+
+
 def test_eager_steps_with_factors(ops):
     """step(factors=...) without a graph, 8 bits: as without factors."""
     n = 700
@@ -153,6 +170,7 @@ def test_refusals(ops):
         opt.step(factors=factors)
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
         b.grad = a.grad
+        a.grad.add_(0)                             # something to capture
         with pytest.raises(ValueError):
             opt.step(factors=factors)              # a second graph with other parameters
     b.grad = None

@@ -49,3 +49,11 @@ def test_size_caches_are_bounded(ops):
             cached(L, M, *args)
         assert cached.cache_info().currsize <= 4096
     assert ops._adapter_workspace.cache_parameters()["maxsize"] == 4096
+
+
+def test_an_optimizer_of_nothing(ops):
+    opt = ops.AdamW([])
+    opt.step()
+    opt.zero_grad()
+    assert opt.counts() == [] and opt.steps == 0
+    opt.load_state_dict(opt.state_dict())
