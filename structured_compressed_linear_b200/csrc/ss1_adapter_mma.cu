@@ -14,7 +14,7 @@
 //
 // Ranks are padded to 16, 32, 64 or 128 (RT). Whole passes, us as graph replays beside what their bytes take at the measured
 // 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 58 (41.7); 16384 x 4096 x 4096: 85 (61.8). Backward, one
-// adapter of 4096 x 4096 x 4096, rank 16: 38 (20.6), rank 64: 55, rank 128: 97; four of 8192 x 768 x 2304, rank 32: 46 (11.9).
+// adapter of 4096 x 4096 x 4096, rank 16: 39.6 (20.6), rank 64: 57, rank 128: 98; four of 8192 x 768 x 2304, rank 32: 47.7 (11.9).
 //
 // P between the kernels: rows in plan order, [2][RT] bf16 each: the value rounded to bf16, and
 // what that left out, rounded again (2^-17 of the value is lost). The products with both parts are
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2) update_kernel(const Update d, Pla
 // 128-byte rows, P's packed rows as boxes of the same kind. The reduction runs over the rows, so both
 // operands of D[column, rank] are read along their rows' contiguous side, as they lie: tcgen05 takes 2 x 128
 // columns x (first parts, second parts) a stage from one thread, and D stays in tensor memory until the
-// run comes to another adapter, when the two parts' sums are added. G and dB in one launch, 4096 x 4096 at rank 16: 17.7 us alone; dA and dX: 20.4
+// run comes to another adapter, when the two parts' sums are added. G and dB in one launch, 4096 x 4096 at rank 16: 18.1 us alone; dA and dX: 21.0
 // (101 MB, 4.9 TB/s). (With mma.sync, whose fragments cost
 // every warp transposed loads and registers, a stage took 1.2 us at rank 32: 29 us for G and dB at
 // 8192 x 2304.) The tiles are dealt evenly whatever their adapters: run k's sums for adapter a go to part[k + a]
