@@ -557,9 +557,9 @@ SS1_API int ss1_adapter_status(int32_t* detail);
  * ss1_test_adapter_timeout -- exercises the time-out path of ss1_adapter_backward without a fault, for tests of
  * failure handling. Runs it (bf16 sizes that its tensor-core kernels take, all three gradients asked for) with
  * every wait cut to limit_ns nanoseconds (1 .. 2e9), while the first CTA of `site` (1 G of the first 128 rows,
- * 2 dB, 3 dA) does not announce the products of its first stage. Its wait runs out, it writes the status word,
- * issues and waits for nothing more, lets what it issued end, frees its tensor memory and leaves NaN: site 1 in the
- * first rows of dX and in dA of their adapters, 2 in dB, 3 in dA. Asynchronous. Errors: as
+ * 2 dB, 3 dA) does not announce the products of its first stage. Its wait runs out, no later one lasts, it
+ * writes the status word, lets what it issued end, frees its tensor memory and leaves NaN: site 1 in the first
+ * rows of dX and in dA of their adapters, 2 in dB, 3 in dA. Asynchronous. Errors: as
  * ss1_adapter_backward; INVALID_ARG (site, limit_ns), UNSUPPORTED_SHAPE (not the tensor-core kernels').
  */
 SS1_API int ss1_test_adapter_timeout(const ss1_adapters* adapters, const void* dY, const void* X, const float* H,

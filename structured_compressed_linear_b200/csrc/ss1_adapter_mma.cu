@@ -14,7 +14,7 @@
 //
 // Ranks are padded to 16, 32, 64 or 128 (RT). Whole passes, us as graph replays beside what their bytes take at the measured
 // 6.55 TB/s. Forward, 4096 x 4096 x 14336, rank 16, eight adapters: 58 (41.7); 16384 x 4096 x 4096: 85 (61.8). Backward, one
-// adapter of 4096 x 4096 x 4096, rank 16: 39.6 (20.6), rank 64: 57, rank 128: 98; four of 8192 x 768 x 2304, rank 32: 47.7 (11.9).
+// adapter of 4096 x 4096 x 4096, rank 16: 39.3 (20.6), rank 64: 57, rank 128: 98; four of 8192 x 768 x 2304, rank 32: 47 (11.9).
 //
 // P between the kernels: rows in plan order, [2][RT] bf16 each: the value rounded to bf16, and
 // what that left out, rounded again (2^-17 of the value is lost). The products with both parts are
@@ -78,9 +78,10 @@ struct Unwatched {
     static constexpr int withhold = 0;
 };
 
-// The tensor core's part of a CTA: one completion barrier a ring slot, and what says that a wait gave up. Then nothing
-// is multiplied or waited for any more, the status word is set, what was issued ends before its memory is freed
-// (or a second limit does), and the CTA's results are NaN.
+// The tensor core's part of a CTA: one completion barrier a ring slot, and what says that a wait gave up. Then no wait of the
+// CTA lasts any more, its results are NaN, the status word is set, and a last commit sees to it that whatever was issued
+// ends before its memory is freed (or a second limit passes). The loops issue as before: a test there of whether to go on cost
+// 2 % (4096 x 4096 x 14336: 67.5 -> 68.8 us).
 constexpr int kSlots = 6;
 __device__ int32_t g_status;      // the first time-out since it was read: kernel id << 8 | 0x80 | site
 struct TensorState {
@@ -103,12 +104,15 @@ __device__ __forceinline__ void tensor_begin(TensorState& t, uint32_t columns) {
     ptx::tc_fence_after();
 }
 __device__ __forceinline__ bool tensor_fine(const TensorState& t) { return *(const volatile int*)&t.gave_up == 0; }
-// False, and the CTA's waits end, where this wait or another one gave up.
 template <typename W>
-__device__ __forceinline__ bool tensor_wait(TensorState& t, int slot, uint32_t parity, const W& watch) {
-    if (ptx::mbar_wait(&t.done[slot], parity, &t.gave_up, watch.limit_ns)) return true;
-    *(volatile int*)&t.gave_up = 1;
-    return false;
+__device__ __forceinline__ void tensor_wait(TensorState& t, int slot, uint32_t parity, const W& watch) {
+    if (!ptx::mbar_wait(&t.done[slot], parity, &t.gave_up, watch.limit_ns)) *(volatile int*)&t.gave_up = 1;
+}
+// One thread; out of line, since small calls wait for their code to be fetched.
+__device__ __noinline__ void tensor_gave_up(TensorState* t, uint64_t limit_ns, int site) {
+    atomicCAS(&g_status, 0, (kStatusKernelAdapter << 8) | 0x80 | site);
+    ptx::umma_commit(&t->done[kSlots - 1]);
+    ptx::mbar_wait(&t->done[kSlots - 1], 0, &t->never, limit_ns);
 }
 // All threads, after the last wait and the last read of tensor memory.
 template <typename W>
@@ -117,11 +121,7 @@ __device__ __forceinline__ void tensor_end(TensorState& t, uint32_t columns, con
     __syncthreads();
     ptx::tc_fence_after();
     if (!tensor_fine(t)) {
-        if (threadIdx.x == 0) {
-            atomicCAS(&g_status, 0, (kStatusKernelAdapter << 8) | 0x80 | site);
-            ptx::umma_commit(&t.done[kSlots - 1]);
-            ptx::mbar_wait(&t.done[kSlots - 1], 0, &t.never, watch.limit_ns);
-        }
+        if (threadIdx.x == 0) tensor_gave_up(&t, watch.limit_ns, site);
         __syncthreads();
     }
     if (threadIdx.x < 32) ptx::tmem_dealloc(t.tmem, columns);
@@ -392,12 +392,12 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
             }
             ptx::tc_fence_before();
         };
-        bool fresh = true, fine = true;     // fine: none of this thread's waits gave up
+        bool fresh = true;
         for (int chunk = from, slot = 0; chunk < to; ++chunk, slot = slot + 1 == kStages ? 0 : slot + 1) {
             ptx::cp_async_wait<kStages - 2>();
             ptx::fence_proxy_async_smem();
             __syncthreads();
-            if (tid == 0 && fine) {
+            if (tid == 0) {
                 const uint32_t su = base + slot * S::stage, stt = su + S::u_bytes;
                 ptx::tc_fence_after();
 #pragma unroll
@@ -407,17 +407,13 @@ __device__ __forceinline__ void products_role(const Products& d, const PlanView&
             }
             fresh = false;
             const int last = slot == 0 ? kStages - 1 : slot - 1;      // the slot of the stage before: loaded again once read
-            if (chunk > from) fine &= tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1, watch);
+            if (chunk > from) tensor_wait(ts, last, ((chunk - 1 - from) / kStages) & 1, watch);
             load(chunk + kStages - 1 < to, last);
-            if ((chunk + 1 - from) % kTakeStages == 0 && chunk + 1 < to) {
-                fine &= tensor_wait(ts, slot, ((chunk - from) / kStages) & 1, watch);
+            if ((chunk + 1 - from) % kTakeStages == 0 || chunk + 1 == to) {
+                tensor_wait(ts, slot, ((chunk - from) / kStages) & 1, watch);
                 take();
                 fresh = true;      // the barrier above comes before the next product overwrites what was read
             }
-        }
-        if (to > from) {
-            tensor_wait(ts, (to - 1 - from) % kStages, ((to - 1 - from) / kStages) & 1, watch);
-            take();
         }
         ptx::cp_async_wait<0>();
         __syncthreads();
@@ -848,13 +844,13 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
     const bool withhold = watch.withhold == site && range == 0 && run == 0;
     constexpr uint32_t kInstr = idesc_mn(2 * RT, true, true);
     const int64_t size = (int64_t)C * R;
-    bool fresh = true, fine = true;        // fine: none of this thread's waits gave up
+    bool fresh = true;
     for (int step = 0, slot = 0;; ++step) {
         if (step % kColSteps == 0 || step == steps) {       // a tile begins, or the run ends
             const int a = step < steps ? next_adapter : -1;
             if (step + kColSteps < steps) next_adapter = tile_of(plan, t0 + step / kColSteps + 1, M).adapter;
             if (a != adapter && (unsigned)adapter < (unsigned)n) {
-                fine &= tensor_wait(ts, slot == 0 ? S::stages - 1 : slot - 1, ((step - 1) / S::stages) & 1, watch);
+                tensor_wait(ts, slot == 0 ? S::stages - 1 : slot - 1, ((step - 1) / S::stages) & 1, watch);
                 ptx::tc_fence_after();
                 const bool valid = tensor_fine(ts);
                 const int2 own = adapter_tiles(plan, adapter, M);
@@ -908,7 +904,7 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
         ptx::cp_async_wait<S::stages - 2>();
         ptx::fence_proxy_async_smem();
         __syncthreads();
-        if (tid == 0 && fine) {
+        if (tid == 0) {
             const uint32_t su = base + slot * S::stage, sp = su + S::u_bytes;
             ptx::tc_fence_after();
 #pragma unroll
@@ -921,7 +917,7 @@ __device__ __forceinline__ void columns_role(const Columns& d, const PlanView& p
         }
         fresh = false;
         const int last = slot == 0 ? S::stages - 1 : slot - 1;        // the slot of the step before: loaded again once read
-        if (step > 0) fine &= tensor_wait(ts, last, ((step - 1) / S::stages) & 1, watch);
+        if (step > 0) tensor_wait(ts, last, ((step - 1) / S::stages) & 1, watch);
         load_u(step + S::stages - 1, last);
         load_p(now, step + S::stages - 1, last);
         advance(step + S::stages - 1);
